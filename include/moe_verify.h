@@ -437,6 +437,165 @@ moe_status moe_verify_rounds(const moe_verify_model* model, const uint16_t* x_ro
  */
 moe_status moe_workspace_error(void* ws, int* code, void* stream);
 
+/*
+ * Serving several sequences: a KV cache in pages, the append of the verify
+ * rows' keys and values to it, the attention of the rows over it, and the
+ * rules a request puts on its logits.
+ *
+ * The rows of a call belong to n_seqs sequences: rows row_start[b] ..
+ * row_start[b + 1] - 1 (device int32 [n_seqs + 1], not decreasing) are
+ * sequence b's, row i of it at position kv_len[b] + i.  A sequence may have
+ * no rows.  Rows before row_start[0] or from row_start[n_seqs] on belong to
+ * no sequence: nothing of theirs is read or written.
+ *
+ * The cache of one layer: position p of sequence b is slot p % page_size of
+ * page table[b * max_pages + p / page_size].  kv_len counts the committed
+ * positions, as in moe_attention_block: the append writes the new rows
+ * behind them, the attention sees them, and moe_kv_commit (on kv_len + b)
+ * counts the accepted ones in.  Entries of the table for pages that hold no
+ * visible position are never read, so they may be anything.  Sequences may
+ * share pages that are only read (a common prompt); a page that rows are
+ * appended to belongs to one sequence.
+ * page_size 16, 32, 64 or 128; head_dim 128; n_seqs 1..1024;
+ * n_pages * nkv * page_size < 2^31.
+ *
+ * What the device finds wrong in a sequence is recorded in the workspace's
+ * error word (moe_workspace_error): MOE_ERR_INVALID_ARG for a page id outside
+ * [0, n_pages), a negative length, or rows outside [0, n_rows) or (attention)
+ * more than max_rows; MOE_ERR_CAPACITY for positions past max_pages *
+ * page_size.  No such call reads or writes out of bounds.
+ */
+typedef struct {
+  uint16_t *kpages, *vpages;  /* bf16 [n_pages][nkv][page_size][128] */
+  const int32_t* table;       /* [n_seqs][max_pages] page ids */
+  const int32_t* kv_len;      /* [n_seqs] committed positions */
+  int n_pages, page_size, nkv, head_dim, n_seqs, max_pages;
+} moe_paged_kv;
+
+/* Bytes of workspace that moe_paged_kv_append and moe_paged_attention of up
+ * to max_rows rows a sequence need (0 on an unsupported shape), zero-filled
+ * once before its first use; calls leave it ready for the next call, of any
+ * smaller shape too.  Zero-fill it again after MOE_ERR_DEVICE_TIMEOUT. */
+size_t moe_paged_workspace_size(int max_rows, int nq, int nkv);
+
+/*
+ * Appends the keys and values of n_rows rows to their sequences' pages, the
+ * queries and keys first turned by the rotary embedding of `pos`
+ * (rotary_dim 0 or pos NULL: not turned; pos->window is not used):
+ *   q, q_out   bf16 [n_rows][nq * 128] or both NULL: the queries and where
+ *              the turned ones go (may be q itself with the same stride)
+ *   k_new, v_new  bf16 [n_rows][nkv * 128]
+ *   *_stride   elements between rows, multiples of 8 (column ranges of one
+ *              fused projection's output need no copy)
+ * The rotation is the attention block's: the angle reduced in double, sine
+ * and cosine in FP32, each product and sum rounded to FP32, one bf16
+ * rounding at the end.
+ * A row whose position has no page (MOE_ERR_CAPACITY) or a page id out of
+ * range is not stored; its query is turned all the same.
+ */
+moe_status moe_paged_kv_append(const moe_paged_kv* kv, const uint16_t* q, int64_t q_stride, const uint16_t* k_new,
+                               int64_t k_stride, const uint16_t* v_new, int64_t v_stride, int n_rows, int nq,
+                               const int32_t* row_start, const moe_attn_pos* pos, uint16_t* q_out,
+                               int64_t q_out_stride, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * What turns q . k into a score, and which positions a row sees.  With
+ * pos the row's position and p the key's:
+ *   s = scale * (q . k)                     (scale 0: 1 / sqrt(128))
+ *   s = softcap * tanh(s / softcap)         if softcap > 0
+ *   s = s + slopes[h] * (p - pos)           if slopes (a bias by distance)
+ *   p is visible if p <= pos, p >= first[b] (a packed document's start; NULL:
+ *   0), and  window == 0  or  p > pos - window  or  p < prefix[b]  (first
+ *   positions that stay visible under the window; NULL: 0)
+ * All zero: plain causal attention.
+ */
+typedef struct {
+  int window;              /* 0: none, else at least 1 */
+  float scale, softcap;    /* finite, not negative */
+  const float* slopes;     /* [nq] or NULL */
+  const int32_t* first;    /* [n_seqs] or NULL */
+  const int32_t* prefix;   /* [n_seqs] or NULL */
+} moe_paged_scores;
+
+/*
+ * Attention of the rows over their sequences' pages (the rows' own keys and
+ * values appended before, see moe_paged_kv_append):
+ *   o[t, h] = bf16( softmax_p( s ) . v_p )  over the visible positions of KV
+ *             head h / (nq / nkv)
+ *   lse[t, h] = ln sum_p exp(s_p)   (optional; -inf for an empty row)
+ * A row that sees no position (or only scores of -inf) gives o = 0.  What
+ * hidden positions hold (NaN and infinities too) changes nothing.
+ *   q  bf16 [n_rows][nq * 128], q_stride elements between rows (a multiple of 8)
+ *   o  bf16 [n_rows][nq * 128], o_stride elements between rows (a multiple of 8)
+ *   lse  float [n_rows][nq] or NULL
+ *   max_rows  no sequence has more rows than this, 1..16;
+ *             max_rows * (nq / nkv) <= 64
+ *   scores  NULL: plain causal attention
+ * A sequence with a wrong length or rows (see above) is skipped, its rows
+ * left as they were; where a page id is out of range the sequence's rows are
+ * undefined.
+ */
+moe_status moe_paged_attention(const moe_paged_kv* kv, const uint16_t* q, int64_t q_stride, int n_rows, int max_rows,
+                               int nq, const int32_t* row_start, const moe_paged_scores* scores, uint16_t* o,
+                               int64_t o_stride, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The lm_head's logits themselves, for rules and samplers that need all of
+ * them: logits[r][v] = x_norm_r . W_v, bit for bit the logits whose argmax
+ * moe_lm_head_argmax takes (shapes, order and workspace as there).
+ *   logits  float [K][V] out
+ */
+moe_status moe_lm_head_logits(const uint16_t* x_norm, int K, int H, const uint16_t* W, int V, float* logits, void* ws,
+                              size_t ws_bytes, void* stream);
+
+/*
+ * The rules of a batch of rows on their logits.  Row r's history is
+ * tokens[begin[r] .. end[r]) (cut to [0, n_tokens); entries outside [0, V)
+ * count for nothing); rows of one drafted block share the tokens and end one
+ * later each.  With c the times v occurs in it, x the logit in FP32, each
+ * operation rounded:
+ *   if c > 0:  x = x > 0 ? x / repetition[r] : x * repetition[r]
+ *              x = x - (presence[r] + c * frequency[r])
+ *   if bias_row[r] >= 0:   x = x + bias[bias_row[r]][v]
+ *   if allow_row[r] >= 0 and bit v % 32 of allow[allow_row[r]][v / 32] is 0:
+ *              x = -inf
+ * A NULL array leaves its rule out (repetition 1, presence and frequency 0).
+ * A bias_row or allow_row at or past n_bias / n_allow counts as negative and
+ * records MOE_ERR_INVALID_ARG.
+ */
+typedef struct {
+  const int32_t *tokens, *begin, *end;                  /* [n_tokens], [R], [R]; or all NULL */
+  int n_tokens;
+  const float *repetition, *presence, *frequency;       /* [R] each, or NULL; repetition > 0 */
+  const float* bias;                                    /* [n_bias][V] or NULL */
+  const int32_t* bias_row;                              /* [R] */
+  int n_bias;
+  const uint32_t* allow;                                /* [n_allow][(V + 31) / 32] or NULL */
+  const int32_t* allow_row;                             /* [R] */
+  int n_allow;
+} moe_logit_rules;
+
+#define MOE_LOGITS_F32 0
+#define MOE_LOGITS_BF16 1
+
+/* Bytes of workspace moe_logits_constrain needs (0 on an unsupported shape);
+ * zero-filled once before first use. */
+size_t moe_logits_workspace_size(int R, int V);
+
+/*
+ * Applies the rules to R rows of logits and takes each row's argmax:
+ *   logits, out  float or bf16 (type MOE_LOGITS_F32 / MOE_LOGITS_BF16)
+ *                [R][V], stride / out_stride elements between rows; out may
+ *                be NULL, or logits itself with the same stride
+ *   tok   int32 [R] or NULL: the argmax of the FP32 values (lowest index on
+ *         a tie, a NaN never); -1 where no token is above -inf
+ *   best  float [R] or NULL: that FP32 value (-inf with tok -1)
+ *   R 1..4096, V 1..2^24; rules NULL: argmax alone.
+ */
+moe_status moe_logits_constrain(const void* logits, int type, int64_t stride, int R, int V,
+                                const moe_logit_rules* rules, void* out, int64_t out_stride, int32_t* tok,
+                                float* best, void* ws, size_t ws_bytes, void* stream);
+
 /* A short English description of a status. */
 const char* moe_status_string(moe_status s);
 

@@ -35,7 +35,9 @@ EXPORTS = ("moe_verify_layer_workspace_size", "moe_router_topk", "moe_group_ints
            "moe_attention_workspace_size", "moe_attention_block", "moe_verify_layer_static",
            "moe_verify_step_workspace_size", "moe_verify_step", "moe_workspace_error", "moe_status_string", "moe_host_pointer",
            "moe_debug_set_wait_limit_ns", "moe_debug_set_trace", "moe_debug_partials_offset", "moe_kv_commit",
-           "moe_synthetic_drafts", "moe_verify_rounds", "moe_dense_mlp_workspace_size", "moe_dense_mlp_block")
+           "moe_synthetic_drafts", "moe_verify_rounds", "moe_dense_mlp_workspace_size", "moe_dense_mlp_block",
+           "moe_paged_workspace_size", "moe_paged_kv_append", "moe_paged_attention", "moe_lm_head_logits",
+           "moe_logits_workspace_size", "moe_logits_constrain")
 
 
 class MoeError(RuntimeError):
@@ -77,6 +79,29 @@ class moe_verify_model(ctypes.Structure):
                 ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("ctx", ctypes.c_int),
                 ("vocab", ctypes.c_int), ("eps", ctypes.c_float), ("layers", ctypes.c_void_p),
                 ("lm_head", ctypes.c_void_p), ("kv_len", ctypes.c_void_p)]
+
+
+MOE_LOGITS_F32 = 0
+MOE_LOGITS_BF16 = 1
+
+
+class moe_paged_kv(ctypes.Structure):
+    _fields_ = [("kpages", ctypes.c_void_p), ("vpages", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("nkv", ctypes.c_int), ("head_dim", ctypes.c_int), ("n_seqs", ctypes.c_int), ("max_pages", ctypes.c_int)]
+
+
+class moe_paged_scores(ctypes.Structure):
+    _fields_ = [("window", ctypes.c_int), ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("slopes", ctypes.c_void_p), ("first", ctypes.c_void_p), ("prefix", ctypes.c_void_p)]
+
+
+class moe_logit_rules(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_void_p), ("begin", ctypes.c_void_p), ("end", ctypes.c_void_p),
+                ("n_tokens", ctypes.c_int), ("repetition", ctypes.c_void_p), ("presence", ctypes.c_void_p),
+                ("frequency", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("bias_row", ctypes.c_void_p),
+                ("n_bias", ctypes.c_int), ("allow", ctypes.c_void_p), ("allow_row", ctypes.c_void_p),
+                ("n_allow", ctypes.c_int)]
 
 
 def _load():
@@ -130,6 +155,19 @@ def _load():
     L.moe_lm_head_workspace_size.argtypes = [ci]
     L.moe_lm_head_argmax.restype = ci
     L.moe_lm_head_argmax.argtypes = [vp, ci, ci, vp, ci, vp, vp, vp, sz, vp]
+    i64 = ctypes.c_int64
+    L.moe_paged_workspace_size.restype = sz
+    L.moe_paged_workspace_size.argtypes = [ci, ci, ci]
+    L.moe_paged_kv_append.restype = ci
+    L.moe_paged_kv_append.argtypes = [vp, vp, i64, vp, i64, vp, i64, ci, ci, vp, vp, vp, i64, vp, sz, vp]
+    L.moe_paged_attention.restype = ci
+    L.moe_paged_attention.argtypes = [vp, vp, i64, ci, ci, ci, vp, vp, vp, i64, vp, vp, sz, vp]
+    L.moe_lm_head_logits.restype = ci
+    L.moe_lm_head_logits.argtypes = [vp, ci, ci, vp, ci, vp, vp, sz, vp]
+    L.moe_logits_workspace_size.restype = sz
+    L.moe_logits_workspace_size.argtypes = [ci, ci]
+    L.moe_logits_constrain.restype = ci
+    L.moe_logits_constrain.argtypes = [vp, ci, i64, ci, ci, vp, vp, i64, vp, vp, vp, sz, vp]
     L.moe_workspace_error.restype = ci
     L.moe_workspace_error.argtypes = [vp, ctypes.POINTER(ctypes.c_int), vp]
     L.moe_status_string.restype = ctypes.c_char_p
@@ -433,6 +471,198 @@ def lm_head_workspace(K: int, device="cuda") -> torch.Tensor:
 def moe_lm_head_argmax(x_norm, W, tok, ws, best_logit=None, stream=None):
     _check(lib.moe_lm_head_argmax(_ptr(x_norm), x_norm.shape[0], x_norm.shape[1], _ptr(W), W.shape[0], _ptr(tok),
                                   _ptr(best_logit), _ptr(ws), ws.numel(), _stream(stream)), "moe_lm_head_argmax")
+
+
+def moe_lm_head_logits(x_norm, W, logits, ws, stream=None):
+    """logits float32 [K, V]: every logit moe_lm_head_argmax chooses from."""
+    _check(lib.moe_lm_head_logits(_ptr(x_norm), x_norm.shape[0], x_norm.shape[1], _ptr(W), W.shape[0], _ptr(logits),
+                                  _ptr(ws), ws.numel(), _stream(stream)), "moe_lm_head_logits")
+
+
+def _like(t, dtype, shape, what, device=None):
+    """Refuses a tensor the library would misread: it sees an address only."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{what} is on {t.device}, not {device}")
+    return t.data_ptr()
+
+
+class PagedKV:
+    """One layer's paged KV cache and its sequences: ``kpages``, ``vpages`` bf16
+    [n_pages, nkv, page_size, 128], ``table`` int32 [n_seqs, max_pages] page
+    ids, ``kv_len`` int32 [n_seqs] committed positions (the layers of a model
+    share the last two).  Keeps the tensors and their C description ``c``."""
+
+    def __init__(self, kpages, vpages, table, kv_len):
+        n, nkv, ps, hd = kpages.shape
+        dev = kpages.device
+        self.kpages, self.vpages, self.table, self.kv_len, self.device = kpages, vpages, table, kv_len, dev
+        self.nkv = nkv
+        self.c = moe_paged_kv(_like(kpages, torch.bfloat16, (n, nkv, ps, hd), "kpages"),
+                              _like(vpages, torch.bfloat16, (n, nkv, ps, hd), "vpages", dev),
+                              _like(table, torch.int32, (kv_len.shape[0], table.shape[1]), "table", dev),
+                              _like(kv_len, torch.int32, (kv_len.shape[0],), "kv_len", dev),
+                              n, ps, nkv, hd, table.shape[0], table.shape[1])
+        self._ref = ctypes.byref(self.c)
+
+
+class PagedScores:
+    """What turns q . k into a score and which positions a row sees
+    (moe_paged_scores).  Keeps its tensors."""
+
+    def __init__(self, window=0, scale=0.0, softcap=0.0, slopes=None, first=None, prefix=None):
+        self.slopes, self.first, self.prefix = slopes, first, prefix
+        self.c = moe_paged_scores(window, scale, softcap,
+                                  _like(slopes, torch.float32, () if slopes is None else (slopes.numel(),), "slopes"),
+                                  _like(first, torch.int32, () if first is None else (first.numel(),), "first"),
+                                  _like(prefix, torch.int32, () if prefix is None else (prefix.numel(),), "prefix"))
+        self._ref = ctypes.byref(self.c)
+
+
+def paged_workspace(kv: PagedKV, max_rows: int, nq: int) -> torch.Tensor:
+    """A zero-filled workspace for appends to ``kv`` and attention of up to
+    ``max_rows`` rows a sequence with ``nq`` query heads."""
+    n = int(lib.moe_paged_workspace_size(max_rows, nq, kv.nkv))
+    if n == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, "paged workspace size")
+    return torch.zeros(n, dtype=torch.uint8, device=kv.device)
+
+
+def _strided(t, what, kv, n_rows, width=None):
+    """(address, row stride) of a row-strided bf16 matrix [n_rows, heads * 128]."""
+    if (t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[0] != n_rows or (width and t.shape[1] != width)
+            or t.stride(1) != 1 or t.device != kv.device):
+        raise ValueError(f"{what} must be a bf16 tensor [{n_rows}, {width or 'heads * 128'}] with unit column stride "
+                         f"on {kv.device}")
+    return t.data_ptr(), t.stride(0)
+
+
+def _starts(kv, row_start):
+    n = kv.c.n_seqs + 1
+    if row_start.dtype != torch.int32 or row_start.shape != (n,) or row_start.device != kv.device or \
+            not row_start.is_contiguous():
+        raise ValueError(f"row_start must be an int32 tensor [{n}] on {kv.device}")
+    return row_start.data_ptr()
+
+
+def _stream_on(device, stream):
+    """The given stream, or the current one of the tensors' device."""
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _heads(t, what):
+    if t.shape[-1] % 128:
+        raise ValueError(f"{what} must have heads * 128 columns")
+    return t.shape[-1] // 128
+
+
+def moe_paged_kv_append(kv: PagedKV, k_new, v_new, row_start, ws, q=None, q_out=None, pos: moe_attn_pos | None = None,
+                        stream=None):
+    """Appends the rows' keys and values (bf16 [T, nkv * 128], rows may be
+    strided) to their sequences' pages and writes the queries to ``q_out``
+    (may be ``q``), queries and keys turned by ``pos``."""
+    T = k_new.shape[0]
+    kp, ks = _strided(k_new, "k_new", kv, T, kv.nkv * 128)
+    vp, vs = _strided(v_new, "v_new", kv, T, kv.nkv * 128)
+    qp = qs = op = os_ = nq = 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        nq = _heads(q, "q")
+        qp, qs = _strided(q, "q", kv, T, nq * 128)
+        op, os_ = _strided(q_out, "q_out", kv, T, nq * 128)
+    with torch.cuda.device(kv.device):
+        _check(lib.moe_paged_kv_append(kv._ref, qp, qs, kp, ks, vp, vs, T, nq, _starts(kv, row_start),
+                                       None if pos is None else ctypes.byref(pos), op, os_, ws.data_ptr(), ws.numel(),
+                                       _stream_on(kv.device, stream)), "moe_paged_kv_append")
+
+
+def moe_paged_attention(kv: PagedKV, q, row_start, o, ws, max_rows, scores: PagedScores | None = None, lse=None,
+                        stream=None):
+    """Attention of the rows (q, o bf16 [T, nq * 128], rows may be strided) over
+    their sequences' pages; ``lse`` float32 [T, nq] or None."""
+    T, nq = q.shape[0], _heads(q, "q")
+    qp, qs = _strided(q, "q", kv, T)
+    op, os_ = _strided(o, "o", kv, T, nq * 128)
+    ref = None
+    if scores is not None:
+        for t, n, what in ((scores.slopes, nq, "slopes"), (scores.first, kv.c.n_seqs, "first"),
+                           (scores.prefix, kv.c.n_seqs, "prefix")):
+            if t is not None and (t.numel() != n or t.device != kv.device):
+                raise ValueError(f"{what} must have {n} values on {kv.device}")
+        ref = scores._ref
+    lp = _like(lse, torch.float32, (T, nq), "lse", kv.device)
+    with torch.cuda.device(kv.device):
+        _check(lib.moe_paged_attention(kv._ref, qp, qs, T, max_rows, nq, _starts(kv, row_start), ref, op, os_, lp,
+                                       ws.data_ptr(), ws.numel(), _stream_on(kv.device, stream)),
+               "moe_paged_attention")
+
+
+class LogitRules:
+    """A batch's rules on its logits (moe_logit_rules).  ``tokens`` int32 with
+    ``begin``, ``end`` int32 [R]; ``repetition``, ``presence``, ``frequency``
+    float32 [R]; ``bias`` float32 [n, V] with ``bias_row`` int32 [R];
+    ``allow`` int32 or uint32 [n, ceil(V / 32)] bit masks with ``allow_row``
+    int32 [R] (rows -1: none).  Keeps its tensors."""
+
+    def __init__(self, tokens=None, begin=None, end=None, repetition=None, presence=None, frequency=None, bias=None,
+                 bias_row=None, allow=None, allow_row=None):
+        self.tensors = dict(tokens=tokens, begin=begin, end=end, repetition=repetition, presence=presence,
+                            frequency=frequency, bias=bias, bias_row=bias_row, allow=allow, allow_row=allow_row)
+        given = [t for t in self.tensors.values() if t is not None]
+        if any(t.device != given[0].device or not t.is_contiguous() for t in given):
+            raise ValueError("the rules' tensors must be contiguous and on one device")
+        rows = {t.numel() for n, t in self.tensors.items()
+                if t is not None and n in ("begin", "end", "repetition", "presence", "frequency", "bias_row", "allow_row")}
+        if len(rows) > 1:
+            raise ValueError("the rules' per-row tensors differ in length")
+        for n, t in self.tensors.items():
+            want = (torch.float32,) if n in ("repetition", "presence", "frequency", "bias") else \
+                (torch.int32, torch.uint32) if n == "allow" else (torch.int32,)
+            if t is not None and t.dtype not in want:
+                raise ValueError(f"{n} must be {want[0]}")
+        self.rows = rows.pop() if rows else None
+        self.device = given[0].device if given else None
+        p = lambda t: None if t is None else t.data_ptr()
+        self.c = moe_logit_rules(p(tokens), p(begin), p(end), 0 if tokens is None else tokens.numel(), p(repetition),
+                                 p(presence), p(frequency), p(bias), p(bias_row), 0 if bias is None else bias.shape[0],
+                                 p(allow), p(allow_row), 0 if allow is None else allow.shape[0])
+        self._ref = ctypes.byref(self.c)
+
+
+def logits_workspace(R: int, V: int, device="cuda") -> torch.Tensor:
+    n = int(lib.moe_logits_workspace_size(R, V))
+    if n == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, "logits workspace size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def moe_logits_constrain(logits, rules: LogitRules | None, ws, out=None, tok=None, best=None, stream=None):
+    """Applies ``rules`` to ``logits`` (float32 or bf16 [R, V], rows may be
+    strided) and takes each row's argmax; ``out`` may be ``logits``."""
+    R, V = logits.shape
+    dev = logits.device
+    if logits.dtype not in (torch.float32, torch.bfloat16) or logits.stride(1) != 1 or not logits.is_cuda:
+        raise ValueError("logits must be a float32 or bf16 CUDA tensor [R, V] with unit column stride")
+    if out is not None and (out.shape != logits.shape or out.dtype != logits.dtype or out.stride(1) != 1 or
+                            out.device != dev):
+        raise ValueError("out must be like logits")
+    ref = None
+    if rules is not None:
+        b, a = rules.tensors["bias"], rules.tensors["allow"]
+        if (rules.rows not in (None, R) or rules.device not in (None, dev) or (b is not None and b.shape[-1] != V) or
+                (a is not None and a.shape[-1] != (V + 31) // 32)):
+            raise ValueError(f"the rules are not for {R} rows of {V} logits on {dev}")
+        ref = rules._ref
+    with torch.cuda.device(dev):
+        _check(lib.moe_logits_constrain(
+            logits.data_ptr(), MOE_LOGITS_BF16 if logits.dtype == torch.bfloat16 else MOE_LOGITS_F32, logits.stride(0),
+            R, V, ref, None if out is None else out.data_ptr(), 0 if out is None else out.stride(0),
+            _like(tok, torch.int32, (R,), "tok", dev), _like(best, torch.float32, (R,), "best", dev), ws.data_ptr(),
+            ws.numel(), _stream_on(dev, stream)), "moe_logits_constrain")
 
 
 def moe_workspace_error(ws, stream=None) -> int:

@@ -413,8 +413,8 @@ size_t moe_lm_head_workspace_size(int K) {
 // lm_head argmax of x (normalised first, in the kernel, when norm_eps > 0).
 static moe_status lm_head_impl(const uint16_t* x_norm, int K, int H, const uint16_t* W, int V, int32_t* tok,
                                float* best_logit, void* ws, size_t ws_bytes, float norm_eps, bool pdl,
-                               int* err, void* stream) {
-  if (!x_norm || !W || !tok || !ws || K < 1 || K > MOE_MAX_ROWS || V < 1) return MOE_ERR_INVALID_ARG;
+                               int* err, void* stream, float* logits = nullptr) {
+  if (!x_norm || !W || (!tok && !logits) || !ws || K < 1 || K > MOE_MAX_ROWS || V < 1) return MOE_ERR_INVALID_ARG;
   if (H < 256 || H % 256 != 0 || H > 2048) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(x_norm) || !aligned16(W) || !aligned16(ws)) return MOE_ERR_MISALIGNED;
   if (ws_bytes < lmhead_ws_bytes(K)) return MOE_ERR_WORKSPACE_TOO_SMALL;
@@ -433,6 +433,7 @@ static moe_status lm_head_impl(const uint16_t* x_norm, int K, int H, const uint1
   a.part_i = reinterpret_cast<int*>(b + 256 + align256(sizeof(float) * kLmMaxGrid * K));
   a.norm_eps = norm_eps;
   a.wait_ns = g_wait_ns.load();
+  a.logits = logits;
   cudaError_t e;
   if (lmhead_stream_fits(K, H)) {
     e = launch_lmhead_stream(a, static_cast<cudaStream_t>(stream), pdl);
@@ -446,6 +447,13 @@ static moe_status lm_head_impl(const uint16_t* x_norm, int K, int H, const uint1
 moe_status moe_lm_head_argmax(const uint16_t* x_norm, int K, int H, const uint16_t* W, int V, int32_t* tok,
                               float* best_logit, void* ws, size_t ws_bytes, void* stream) {
   return lm_head_impl(x_norm, K, H, W, V, tok, best_logit, ws, ws_bytes, 0.f, false, nullptr, stream);
+}
+
+moe_status moe_lm_head_logits(const uint16_t* x_norm, int K, int H, const uint16_t* W, int V, float* logits, void* ws,
+                              size_t ws_bytes, void* stream) {
+  if (!logits) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(logits)) return MOE_ERR_MISALIGNED;
+  return lm_head_impl(x_norm, K, H, W, V, nullptr, nullptr, ws, ws_bytes, 0.f, false, nullptr, stream, logits);
 }
 
 struct AttnLayout {
@@ -481,7 +489,9 @@ static moe_status check_attn(int K, int H, int nq, int nkv, int hd, int C) {
   return MOE_OK;
 }
 
-static moe_status check_pos(const moe_attn_pos* p) {
+}  // extern "C"
+
+moe_status moe::check_pos(const moe_attn_pos* p) {
   if (!p) return MOE_OK;
   if (p->window < 0 || (p->window > 0 && p->window < 16)) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (p->rotary_dim < 0 || p->rotary_dim > 128 || p->rotary_dim % 2 != 0) return MOE_ERR_UNSUPPORTED_SHAPE;
@@ -492,7 +502,7 @@ static moe_status check_pos(const moe_attn_pos* p) {
 
 // Angle per position of each rotary pair (YaRN-scaled when asked) and the
 // logit temperature.
-static void rope_freqs(const moe_attn_pos& p, double* f, double* temp) {
+void moe::rope_freqs(const moe_attn_pos& p, double* f, double* temp) {
   const double two_pi = 6.283185307179586476925286766559;
   const int rd = p.rotary_dim;
   const bool yarn = p.yarn_factor > 1.f;
@@ -509,6 +519,10 @@ static void rope_freqs(const moe_attn_pos& p, double* f, double* temp) {
   const double m = yarn ? 0.1 * std::log((double)p.yarn_factor) + 1.0 : 1.0;
   *temp = m * m;
 }
+
+uint64_t moe::wait_limit_ns() { return g_wait_ns.load(); }
+
+extern "C" {
 
 size_t moe_attention_workspace_size(int K, int H, int nq, int nkv, int head_dim) {
   if (check_attn(K, H, nq, nkv, head_dim, 0) != MOE_OK) return 0;

@@ -194,6 +194,7 @@ struct LmHeadArgs {
   int rows_per_stage; // streamed kernel (set by its launcher)
   int* err;           // streamed kernel: a ring wait that ran out, or null
   uint64_t wait_ns;
+  float* logits;      // [K][V] out instead of the argmax, or null
 };
 
 constexpr int kLmMaxGrid = 1024;
@@ -321,6 +322,68 @@ cudaError_t launch_kv_commit(int32_t* len, const int32_t* n_accepted, int K, int
 cudaError_t launch_stage_rows(const void* src, void* dst, size_t bytes, cudaStream_t s);
 cudaError_t launch_synthetic_drafts(const int32_t* target, const uint8_t* coin, const int32_t* alt, int K, int vocab,
                                     int32_t* draft, cudaStream_t s);
+
+// ------------------------------------------------------------------ serving (paged.cu, logits.cu, serve_capi.cu)
+constexpr int kPagedMaxSeqs = 1024;
+constexpr int kPagedMaxCtas = 320;  // CTAs of the paged attention (partials and join counters are per CTA)
+
+// A paged cache and the rows of a call (see moe_paged_kv in the header).
+struct PagedRows {
+  uint16_t *kp, *vp;       // [n_pages][nkv][1 << lps][128]
+  const int32_t* table;    // [n_seqs][max_pages]
+  const int32_t* kv_len;   // [n_seqs]
+  const int32_t* start;    // [n_seqs + 1]
+  int n_pages, lps, nkv, n_seqs, max_pages, T;
+  int* err;
+};
+
+struct PagedAppendArgs {
+  PagedRows p;
+  const uint16_t *q, *k, *v;  // q null: keys and values only
+  uint16_t* qo;
+  int64_t qs, ks, vs, qos;    // row strides
+  int nq, rd;                 // rd: rotary dims (0: none)
+  int rows;                   // rows per CTA (set by the launcher)
+  double freq[64];            // angle per position of pair i
+};
+cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s);
+
+struct PagedAttnArgs {
+  PagedRows p;
+  const uint16_t* q;
+  uint16_t* o;
+  float* lse;
+  int64_t qs, os;
+  int nq, group, max_rows;
+  int window;
+  float scale;                // of q . k
+  float softcap;              // 0: none
+  const float* slopes;
+  const int32_t *first, *prefix;
+};
+cudaError_t launch_paged_attention(const PagedAttnArgs& a, cudaStream_t s);
+
+struct LogitArgs {
+  const void* x;
+  void* out;
+  int64_t xs, os;             // row strides
+  int bf16, R, V;
+  moe_logit_rules rules;
+  int32_t* tok;
+  float* best;
+  int tile, ntile;            // tokens per CTA, CTAs per row (set by the launcher)
+  int* err;
+  unsigned* ticket;           // [R]
+  float* part_v;              // [R][kLogitMaxTiles]
+  int* part_i;
+};
+constexpr int kLogitTile = 8192;  // most tokens of a CTA
+cudaError_t launch_logits(const LogitArgs& a, cudaStream_t s);
+
+// capi.cu: the limit of device waits; the angles and temperature of a moe_attn_pos
+uint64_t wait_limit_ns();
+void rope_freqs(const moe_attn_pos& p, double* f, double* temp);
+moe_status check_pos(const moe_attn_pos* p);
 
 int num_sms();
 

@@ -1,0 +1,417 @@
+"""The paged append and attention on the GPU against their 64-bit definition:
+lengths around every tile and page edge, empty rows and sequences, score
+forms, strides, hidden NaNs, bad pages, graphs, streams and workspaces."""
+import math
+
+import pytest
+import torch
+
+import paged_ref as ref
+
+pytestmark = pytest.mark.gpu
+HD = 128
+
+
+@pytest.fixture(scope="module")
+def M(cuda_ok):
+    import moe_nvfp4_block_gb300 as M
+    return M
+
+
+def queries(t, nq, seed, strided=False, scale=2.0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    q = (scale * torch.randn(t, (nq + 3 if strided else nq) * HD, generator=g, device="cuda")).bfloat16()
+    return q[:, HD:(nq + 1) * HD] if strided else q
+
+
+def run(M, k, v, table, n, start, q, nq, max_rows, strided=False, ws=None, stream=None, **kw):
+    kv = M.PagedKV(k, v, table, n)
+    t = q.shape[0]
+    o = torch.full((t, (nq + 2 if strided else nq) * HD), 7.0, dtype=torch.bfloat16, device="cuda")
+    o = o[:, HD:(nq + 1) * HD] if strided else o
+    lse = torch.full((t, nq), 7.0, device="cuda")
+    ws = ws if ws is not None else M.paged_workspace(kv, max_rows, nq)
+    M.moe_paged_attention(kv, q, start, o, ws, max_rows, scores=M.PagedScores(**kw) if kw else None, lse=lse,
+                          stream=stream)
+    return o, lse, ws
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def check(M, lens, rows, nq, nkv, ps, seed=0, max_rows=None, strided=False, fill=float("nan"), first=None, prefix=None,
+          **kw):
+    k, v, table, n, start = ref.make_cache(lens, rows, nkv, ps, seed, fill=fill)
+    q = queries(sum(rows), nq, seed + 1, strided)
+    dev = dict(kw)
+    if first:
+        dev["first"] = ints(first)
+    if prefix:
+        dev["prefix"] = ints(prefix)
+    o, lse, ws = run(M, k, v, table, n, start, q, nq, max_rows or max(rows), strided, **dev)
+    assert M.moe_workspace_error(ws) == 0
+    want = ref.attention(q, k, v, table, lens, rows, nq, first=first, prefix=prefix, **kw)
+    ref.check_attention(o, lse, want, f"lens {lens} rows {rows} heads {nq}/{nkv} page {ps} {kw}")
+
+
+@pytest.mark.parametrize("ps", [16, 32, 64, 128])
+@pytest.mark.parametrize("nq,nkv,rows", [(8, 2, [1] * 9), (4, 4, [3, 1, 2, 0, 4, 1, 1, 2, 3]), (16, 2, [4] * 9),
+                                         (8, 1, [8, 1, 5, 0, 7, 2, 8, 3, 6]), (16, 4, [16] * 9)])
+def test_lengths_around_tiles_and_pages(M, nq, nkv, rows, ps):
+    check(M, [0, 1, 15, 16, 47, 63, 64, 130, 255], rows, nq, nkv, ps, seed=ps + nq)
+
+
+def test_one_token_of_an_empty_cache(M):
+    check(M, [0], [1], 2, 1, 16)
+
+
+@pytest.mark.parametrize("lens,rows", [([5000], [1]), ([3000, 1, 20000], [4, 4, 2]), ([100] * 40, [2] * 40),
+                                       ([9000, 0, 0, 700], [0, 16, 0, 16])])
+def test_long_and_unequal_lengths(M, lens, rows):
+    check(M, lens, rows, 8, 2, 64, seed=3)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(window=1), dict(window=5), dict(window=64), dict(window=200), dict(window=10**6), dict(softcap=5.0),
+    dict(softcap=30.0, window=33), dict(scale=0.02), dict(window=17, prefix=[0, 3, 100, 17, 2000]),
+    dict(first=[0, 70, 5, 64, 1000]), dict(first=[3, 2, 129, 0, 900], window=40, prefix=[10, 1, 140, 9, 901])])
+@pytest.mark.parametrize("rows,nq,nkv", [([2, 1, 4, 3, 4], 8, 2), ([1] * 5, 4, 4), ([8, 7, 3, 8, 1], 8, 1)])
+def test_score_forms(M, kw, rows, nq, nkv):
+    check(M, [3, 77, 200, 64, 1100], rows, nq, nkv, 32, seed=5, **kw)
+
+
+@pytest.mark.parametrize("rows", [[2, 1, 3], [1, 1, 1]])
+def test_distance_bias(M, rows):
+    slopes = 2.0 ** -torch.arange(1, 9, device="cuda").float()
+    check(M, [500, 20, 3000], rows, 8, 4, 16, seed=6, slopes=slopes)
+    check(M, [500, 20, 3000], rows, 8, 4, 16, seed=6, slopes=-slopes / 64, softcap=20.0, window=300)
+
+
+def test_rows_that_see_nothing(M):
+    # first past the rows' positions: o = 0, lse = -inf; some rows of a sequence only
+    check(M, [10, 40, 5, 300], [3, 2, 4, 1], 8, 2, 16, first=[11, 1000, 7, 2**31 - 1])
+
+
+def test_strided_rows(M):
+    check(M, [33, 129], [4, 3], 8, 2, 64, strided=True)
+
+
+@pytest.mark.parametrize("fill", [0.0, float("inf"), float("-inf"), 3e38])
+def test_hidden_slots_hold_anything(M, fill):
+    check(M, [17, 90, 64], [2, 5, 1], 4, 2, 32, fill=fill, window=30)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("window", [0, 20])
+def test_a_rows_own_bad_value_stays_its_own(M, bad, window):
+    # position 100 + 2 (row 2's own) holds a bad value, hidden from rows 0 and 1; with the
+    # window position 85 too is hidden from rows 5 on
+    lens, rows, nq, nkv = [100], [8], 8, 1
+    k, v, table, n, start = ref.make_cache(lens, rows, nkv, 16, 1, fill=float("nan"))
+    for p in (102, 85) if window else (102,):
+        v[table[0, p // 16].long(), 0, p % 16, 5:9] = bad
+    q = queries(8, nq, 2)
+    o, lse, _ = run(M, k, v, table, n, start, q, nq, 8, window=window)
+    ro, rl, _ = ref.attention(q, k, v, table, lens, rows, nq, window=window)
+    got = o.double().reshape(ro.shape)
+    fine = torch.isfinite(ro)
+    assert bool((torch.isfinite(got) == fine).all())
+    assert bool(fine[:2].all()) if not window else bool(fine[6:, :, :5].all())
+    d = (got - ro)[fine].abs()
+    assert bool((d <= 2.0 ** -8 * ro[fine].abs() + 2.0 ** -11 * 4).all())
+    assert bool(torch.isfinite(lse).all())
+
+
+def test_keys_of_infinite_score(M):
+    # a visible score of -inf counts for nothing; all of them: an empty row
+    k, v, table, n, start = ref.make_cache([2], [1], 1, 16, 1)
+    page = table[0, 0].long()
+    k[page, 0, :2] = 0
+    k[page, 0, :2, 0] = float("-inf")
+    q = torch.ones(1, HD, dtype=torch.bfloat16, device="cuda")
+    o, lse, _ = run(M, k, v, table, n, start, q, 1, 1)
+    assert torch.equal(o[0], v[page, 0, 2])
+    k[page, 0, 2] = k[page, 0, 1]
+    o, lse, _ = run(M, k, v, table, n, start, q, 1, 1)
+    assert bool((o == 0).all()) and bool((lse == -math.inf).all())
+
+
+def test_rows_of_no_sequence_are_left_alone(M):
+    k, v, table, n, start = ref.make_cache([40, 9], [2, 1], 2, 16, 0)
+    q = queries(8, 4, 1)
+    o, lse, ws = run(M, k, v, table, n, start + 2, q, 4, 2)
+    want = ref.attention(q[2:5], k, v, table, [40, 9], [2, 1], 4)
+    ref.check_attention(o[2:5], lse[2:5], want)
+    for x in (o, lse):
+        assert bool((x[:2] == 7).all()) and bool((x[5:] == 7).all())
+    assert M.moe_workspace_error(ws) == 0
+
+
+def test_shared_prompt_pages(M):
+    k, v, table, n, start = ref.make_cache([64, 70], [1, 1], 2, 32, 0)
+    table[1, :2] = table[0, :2]
+    q = queries(2, 4, 1)
+    o, lse, _ = run(M, k, v, table, n, start, q, 4, 1)
+    ref.check_attention(o, lse, ref.attention(q, k, v, table, [64, 70], [1, 1], 4))
+
+
+def test_wrong_sequences_are_skipped_and_recorded(M):
+    lens, rows = [40, 30, 20], [1, 2, 1]
+    k, v, table, n, start = ref.make_cache(lens, rows, 2, 16, 0, spare=0)
+    q = queries(4, 4, 1)
+    want = ref.attention(q, k, v, table, lens, rows, 4)
+    for what, code in (("negative", M.MOE_ERR_INVALID_ARG), ("long", M.MOE_ERR_CAPACITY), ("huge", M.MOE_ERR_CAPACITY),
+                       ("rows", M.MOE_ERR_INVALID_ARG), ("outside", M.MOE_ERR_INVALID_ARG)):
+        m, s, mr = n.clone(), start.clone(), 2
+        if what == "rows":
+            mr = 1
+        elif what == "outside":
+            s[1] = -1
+        else:
+            m[1] = {"negative": -1, "long": 16 * table.shape[1] - 1, "huge": 2**31 - 1}[what]
+        o, lse, ws = run(M, k, v, table, m, s, q, 4, mr)
+        assert M.moe_workspace_error(ws) == code, what
+        assert M.moe_workspace_error(ws) == 0
+        skipped = slice(1, 3)
+        if what != "outside":
+            assert bool((o[skipped] == 7).all()) and bool((lse[skipped] == 7).all())
+            ref.check_attention(o[:1], lse[:1], [x[:1] for x in want])
+        ref.check_attention(o[3:], lse[3:], [x[3:] for x in want])
+        o, lse, _ = run(M, k, v, table, n, start, q, 4, 2, ws=ws)  # the workspace stays usable
+        ref.check_attention(o, lse, want)
+
+
+@pytest.mark.parametrize("page", [-1, 10**6, 2**31 - 1, -2**31])
+def test_bad_page_ids_are_recorded(M, page):
+    lens, rows = [40, 50], [1, 2]
+    k, v, table, n, start = ref.make_cache(lens, rows, 2, 16, 0)
+    q = queries(3, 4, 1)
+    want = ref.attention(q, k, v, table, lens, rows, 4)
+    bad = table.clone()
+    bad[0, 1] = page
+    o, lse, ws = run(M, k, v, bad, n, start, q, 4, 2)
+    assert M.moe_workspace_error(ws) == M.MOE_ERR_INVALID_ARG
+    ref.check_attention(o[1:], lse[1:], [x[1:] for x in want])
+    # a page that holds no visible position is not looked at
+    o, lse, ws = run(M, k, v, bad, n, start, q, 4, 2, window=5)
+    assert M.moe_workspace_error(ws) == 0
+    ref.check_attention(o, lse, ref.attention(q, k, v, table, lens, rows, 4, window=5))
+
+
+def test_same_bits_again_in_any_workspace(M):
+    lens, rows = [7000, 300, 4000], [4, 2, 4]
+    k, v, table, n, start = ref.make_cache(lens, rows, 4, 32, 0)
+    q = queries(10, 16, 1)
+    o, lse, ws = run(M, k, v, table, n, start, q, 16, 4)
+    big = M.paged_workspace(M.PagedKV(k, v, table, n), 16, 16)
+    big[512 + 4 * 320:].random_(0, 255)  # partials of another shape
+    for w in (ws, ws, big, big):
+        o2, lse2, _ = run(M, k, v, table, n, start, q, 16, 4, ws=w)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_graph_replay_follows_the_lengths(M):
+    lens, rows = [700, 30], [2, 2]
+    k, v, table, n, start = ref.make_cache([l + 600 for l in lens], rows, 2, 64, 0)
+    kv = M.PagedKV(k, v, table, n)
+    q, o, lse = queries(4, 8, 1), torch.zeros(4, 8 * HD, dtype=torch.bfloat16, device="cuda"), torch.zeros(4, 8, device="cuda")
+    ws = M.paged_workspace(kv, 2, 8)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        M.moe_paged_attention(kv, q, start, o, ws, 2, lse=lse)
+    side.synchronize()
+    graphs = []
+    for _ in range(2):  # two graphs, one workspace
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            M.moe_paged_attention(kv, q, start, o, ws, 2, lse=lse)
+    for step, add in enumerate((0, 1, 64, 555)):
+        n.copy_(ints([l + add for l in lens]))
+        graphs[step % 2].replay()
+        torch.cuda.synchronize()
+        ref.check_attention(o, lse, ref.attention(q, k, v, table, [l + add for l in lens], rows, 8))
+
+
+def test_another_stream(M):
+    lens, rows = [500, 30], [2, 1]
+    k, v, table, n, start = ref.make_cache(lens, rows, 2, 64, 0)
+    q = queries(3, 8, 1)
+    want = ref.attention(q, k, v, table, lens, rows, 8)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        o, lse, _ = run(M, k, v, table, n, start, q, 8, 2)
+        ref.check_attention(o, lse, want)
+    kv, o2 = M.PagedKV(k, v, table, n), torch.zeros_like(o)
+    ws = M.paged_workspace(kv, 2, 8)
+    torch.cuda.synchronize()
+    M.moe_paged_attention(kv, q, start, o2, ws, 2, stream=s)
+    s.synchronize()
+    assert torch.equal(o, o2)
+
+
+def test_offsets_past_32_bits(M):
+    # a pool of 2^31 + elements: the last pages lie past 2^32 bytes and 2^31 elements
+    nkv, ps = 8, 128
+    pages = 2**31 // (nkv * ps * HD) + 40
+    k, v = (torch.zeros(pages, nkv, ps, HD, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table = torch.arange(pages - 6, pages, dtype=torch.int32, device="cuda").reshape(2, 3)
+    k[pages - 6:].normal_()
+    v[pages - 6:].normal_()
+    n, start = ints([300, 200]), ints([0, 1, 3])
+    q = queries(3, 8, 1)
+    o, lse, _ = run(M, k, v, table, n, start, q, 8, 2)
+    ref.check_attention(o, lse, ref.attention(q, k, v, table, [300, 200], [1, 2], 8))
+    kv = M.PagedKV(k, v, table, n)
+    rows = torch.randn(3, nkv * HD, device="cuda").bfloat16()
+    M.moe_paged_kv_append(kv, rows, -rows, start, M.paged_workspace(kv, 1, 8))
+    assert torch.equal(k[pages - 6 + 2, :, 300 - 256].reshape(-1), rows[0])
+    assert torch.equal(v[pages - 6 + 4, :, 201 - 128].reshape(-1), -rows[2])
+
+
+# ---------------------------------------------------------------- append
+
+def append_case(M, lens, rows, nq, nkv, ps, rd=0, theta=10000.0, yarn=0.0, in_place=False, with_q=True, lead=0, seed=0):
+    k, v, table, n, start = ref.make_cache(lens, rows, nkv, ps, seed)
+    t = sum(rows) + 2 * lead
+    start = start + lead
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed + 1)
+    qkv = torch.randn(t, (nq + 2 * nkv + 1) * HD, generator=g, device="cuda").bfloat16()
+    q, kn, vn = qkv[:, :nq * HD], qkv[:, nq * HD:(nq + nkv) * HD], qkv[:, (nq + nkv) * HD:(nq + 2 * nkv) * HD]
+    q0, k0, v0, was_k, was_v = q.clone(), kn.clone(), vn.clone(), k.clone(), v.clone()
+    kv = M.PagedKV(k, v, table, n)
+    ws = M.paged_workspace(kv, 1, nkv)
+    pos = M.attn_pos(rotary_dim=rd, rope_theta=theta, yarn_factor=yarn, yarn_orig_ctx=4096)
+    out = (q if in_place else torch.full((t, nq * HD), 7.0, dtype=torch.bfloat16, device="cuda")) if with_q else None
+    M.moe_paged_kv_append(kv, kn, vn, start, ws, q=q if with_q else None, q_out=out, pos=pos)
+    torch.cuda.synchronize()
+    assert M.moe_workspace_error(ws) == 0
+    at = torch.cat([torch.arange(r, device="cuda") + l for l, r in zip(lens, rows)]) if sum(rows) else ints([]).long()
+    b = torch.tensor([i for i, r in enumerate(rows) for _ in range(r)], device="cuda", dtype=torch.long)
+    f = ref.rotary_freqs(rd, theta, yarn, 4096)
+    live = slice(lead, t - lead)
+    want_q = ref.rotate(q0[live].double().unflatten(1, (-1, HD)), at, f)
+    want_k = ref.rotate(k0[live].double().unflatten(1, (-1, HD)), at, f)
+    page, slot = table[b, at // ps].long(), at % ps
+    # half a bf16 step, and the FP32 work before it: cos and sin to 2^-22, three roundings of values up to |x| + |y|
+    near = lambda got, want: bool(((got.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -20 * 16).all())
+    assert near(k[page, :, slot], want_k)
+    assert torch.equal(v[page, :, slot], v0[live].unflatten(1, (-1, HD)))
+    if rd == 0:
+        assert torch.equal(k[page, :, slot], k0[live].unflatten(1, (-1, HD)))
+    if with_q:
+        assert near(out[live].unflatten(1, (-1, HD)), want_q)
+        for edge in (slice(0, lead), slice(t - lead, t)):
+            assert torch.equal(out[edge], q0[edge] if in_place else torch.full_like(out[edge], 7.0))
+    # nothing else changed
+    k[page, :, slot] = was_k[page, :, slot]
+    v[page, :, slot] = was_v[page, :, slot]
+    assert torch.equal(k, was_k) and torch.equal(v, was_v)
+
+
+@pytest.mark.parametrize("rd", [0, 2, 16, 20, 32, 64, 96, 126, 128])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_append_rotary_widths(M, rd, in_place):
+    append_case(M, [0, 15, 100, 16383], [1, 4, 0, 3], 4, 2, 16, rd=rd, in_place=in_place, lead=1)
+
+
+@pytest.mark.parametrize("ps", [16, 32, 64, 128])
+def test_append_page_sizes_and_yarn(M, ps):
+    append_case(M, [63, 64, 1, 127, 200000], [3, 2, 140, 1, 5], 6, 3, ps, rd=64, theta=500000.0, yarn=4.0)
+
+
+def test_append_without_queries(M):
+    append_case(M, [5, 50], [2, 1], 4, 1, 16, rd=128, with_q=False)
+
+
+@pytest.mark.parametrize("rows", [[1], [1500, 301], [700] * 4, [1] * 1024])
+def test_append_many_rows(M, rows):
+    append_case(M, [(i * 37) % 90 for i in range(len(rows))], rows, 2, 1, 32, rd=128)
+
+
+def test_append_past_the_pages_is_recorded(M):
+    lens, rows = [30, 10, 5], [4, 2, 3]
+    k, v, table, n, start = ref.make_cache(lens, rows, 1, 16, 0, spare=0)
+    table = table[:, :2].contiguous()   # two pages: position 32 and on have none
+    table[1, 0] = -3
+    n[2] = -1
+    was_k = k.clone()
+    kv = M.PagedKV(k, v, table, n)
+    rows_ = torch.randn(9, HD, device="cuda").bfloat16()
+    ws = M.paged_workspace(kv, 1, 1)
+    M.moe_paged_kv_append(kv, rows_, rows_, start, ws)
+    assert M.moe_workspace_error(ws) in (M.MOE_ERR_CAPACITY, M.MOE_ERR_INVALID_ARG)
+    p = table[0, 1].long()
+    assert torch.equal(k[p, 0, 14:16], rows_[:2])
+    k[p, 0, 14:16] = was_k[p, 0, 14:16]
+    assert torch.equal(k, was_k)
+
+
+# ---------------------------------------------------------------- together
+
+def test_a_verify_loop_over_pages(M):
+    """Rounds of a batch as a server runs them: project, append with rotary
+    positions, attend, lm_head logits under rules, accepted prefix, commit."""
+    H, nq, nkv, V, K, ps = 256, 4, 2, 1003, 4, 16
+    lens = [5, 30, 0]
+    B, T = len(lens), len(lens) * K
+    k, v, table, n, start = ref.make_cache([l + 60 for l in lens], [K] * B, nkv, ps, 0)
+    n.copy_(ints(lens))
+    kv = M.PagedKV(k, v, table, n)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    w_qkv = (torch.randn(H, (nq + 2 * nkv) * HD, generator=g, device="cuda") / 16).bfloat16()
+    w_o = (torch.randn(nq * HD, H, generator=g, device="cuda") / 22).bfloat16()
+    w_v = (torch.randn(V, H, generator=g, device="cuda") / 16).bfloat16()
+    pos = M.attn_pos(rotary_dim=128)
+    ws, lws, hws = M.paged_workspace(kv, K, nq), M.logits_workspace(T, V), M.lm_head_workspace(T)
+    freq = ref.rotary_freqs(128, 10000.0)
+    tokens = torch.randint(0, V, (B * 200,), generator=g, device="cuda", dtype=torch.int32)
+    shadow = [[], [], []]  # committed (rotated) keys and values of every sequence, from the cache itself
+    for rnd in range(3):
+        x = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+        qkv = x @ w_qkv
+        q = torch.empty(T, nq * HD, dtype=torch.bfloat16, device="cuda")
+        a, b = nq * HD, (nq + nkv) * HD
+        before = n.tolist()
+        M.moe_paged_kv_append(kv, qkv[:, a:b], qkv[:, b:], start, ws, q=qkv[:, :a], q_out=q, pos=pos)
+        o = torch.empty_like(q)
+        M.moe_paged_attention(kv, q, start, o, ws, K)
+        h = x + o @ w_o
+        logits = torch.empty(T, V, device="cuda")
+        M.moe_lm_head_logits(h, w_v, logits, hws)
+        rules = M.LogitRules(tokens=tokens, begin=ints([i // K * 200 for i in range(T)]),
+                             end=ints([i // K * 200 + 50 + i % K for i in range(T)]),
+                             repetition=torch.full((T,), 1.2, device="cuda"))
+        target = torch.empty(T, dtype=torch.int32, device="cuda")
+        M.moe_logits_constrain(logits, rules, lws, out=logits, tok=target)
+        draft = target.clone()
+        draft[1] = -5         # sequence 0 accepts one draft, sequence 1 all, sequence 2 none
+        draft[2 * K] = -5
+        acc = torch.empty(B, dtype=torch.int32, device="cuda")
+        for s in range(B):
+            M.verify_accept_prefix(draft[s * K:(s + 1) * K], target[s * K:(s + 1) * K], acc[s:])
+            M.moe_kv_commit(n[s:], acc[s:], K, 10**6)
+        torch.cuda.synchronize()
+        assert acc.tolist() == [1, K, 0]
+        assert n.tolist() == [before[0] + 2, before[1] + K, before[2] + 1]
+        at = torch.tensor([l + i for l in before for i in range(K)], device="cuda")
+        want_q = ref.rotate(qkv[:, :a].double().unflatten(1, (-1, HD)), at, freq)
+        assert bool(((q.double().unflatten(1, (-1, HD)) - want_q).abs() <= 2.0 ** -8 * want_q.abs() + 2.0 ** -16).all())
+        ref.check_attention(o, None, ref.attention(q, k, v, table, before, [K] * B, nq), f"round {rnd}")
+        out, tok, _ = ref.logits((h.double() @ w_v.double().T).float().cpu(), tokens.cpu(),
+                                 [i // K * 200 for i in range(T)], [i // K * 200 + 50 + i % K for i in range(T)],
+                                 torch.full((T,), 1.2))
+        assert bool((logits.cpu() - out).abs().max() <= 1e-4)
+        for s in range(B):  # what was committed stays where it is
+            for p, (kk, vv) in enumerate(shadow[s]):
+                page, slot = table[s, p // ps].long(), p % ps
+                assert torch.equal(k[page, :, slot], kk) and torch.equal(v[page, :, slot], vv)
+            for p in range(len(shadow[s]), int(n[s])):
+                page, slot = table[s, p // ps].long(), p % ps
+                shadow[s].append((k[page, :, slot].clone(), v[page, :, slot].clone()))
+    for w in (ws, lws, hws):
+        assert M.moe_workspace_error(w) == 0
