@@ -361,7 +361,18 @@ struct PagedAttnArgs {
   const float* slopes;
   const int32_t *first, *prefix;
 };
-cudaError_t launch_paged_attention(const PagedAttnArgs& a, cudaStream_t s);
+// The kernel's arguments: the pages as bf16 tensor maps over [n_pages * nkv *
+// page_size rows][128 dims] (encode_page_map).
+struct PagedAttnParams {
+  PagedAttnArgs a;
+  CUtensorMap km, vm;
+  unsigned* count;  // [kPagedMaxCtas] parts of a cut unit that arrived, zero between calls
+  float* part_o;    // [kPagedMaxCtas][2][padded rows][128]
+  float* part_ml;   // [kPagedMaxCtas][2][padded rows][2]
+  uint64_t wait_ns;
+};
+bool encode_page_map(CUtensorMap* m, const uint16_t* pages, int64_t rows, int box_rows);
+cudaError_t launch_paged_attention(const PagedAttnParams& a, cudaStream_t s);
 
 struct LogitArgs {
   const void* x;

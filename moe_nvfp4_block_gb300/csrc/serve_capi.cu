@@ -157,7 +157,8 @@ moe_status moe_paged_kv_append(const moe_paged_kv* kv, const uint16_t* q, int64_
 moe_status moe_paged_attention(const moe_paged_kv* kv, const uint16_t* q, int64_t q_stride, int n_rows, int max_rows,
                                int nq, const int32_t* row_start, const moe_paged_scores* scores, uint16_t* o,
                                int64_t o_stride, float* lse, void* ws, size_t ws_bytes, void* stream) {
-  PagedAttnArgs a{};
+  PagedAttnParams A{};
+  PagedAttnArgs& a = A.a;
   moe_status st = paged_rows(kv, n_rows, row_start, ws, &a.p);
   if (st != MOE_OK) return st;
   if ((st = check_heads(max_rows, nq, kv->nkv)) != MOE_OK) return st;
@@ -188,7 +189,16 @@ moe_status moe_paged_attention(const moe_paged_kv* kv, const uint16_t* q, int64_
   a.slopes = scores->slopes;
   a.first = scores->first;
   a.prefix = scores->prefix;
-  return launch_paged_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  char* b = static_cast<char*>(ws);
+  A.count = reinterpret_cast<unsigned*>(b + L.count);
+  A.part_ml = reinterpret_cast<float*>(b + L.part_ml);
+  A.part_o = reinterpret_cast<float*>(b + L.part_o);
+  A.wait_ns = wait_limit_ns();
+  const int64_t rows = (int64_t)kv->n_pages * kv->nkv * kv->page_size;
+  const int box = kv->page_size < 64 ? kv->page_size : 64;
+  if (!encode_page_map(&A.km, kv->kpages, rows, box) || !encode_page_map(&A.vm, kv->vpages, rows, box))
+    return MOE_ERR_CUDA;
+  return launch_paged_attention(A, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 size_t moe_logits_workspace_size(int R, int V) {

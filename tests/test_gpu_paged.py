@@ -415,3 +415,25 @@ def test_a_verify_loop_over_pages(M):
                 shadow[s].append((k[page, :, slot].clone(), v[page, :, slot].clone()))
     for w in (ws, lws, hws):
         assert M.moe_workspace_error(w) == 0
+
+
+@pytest.mark.parametrize("nq,rows", [(8, [1, 2]), (8, [4, 8])])
+def test_wait_limit_is_recorded_and_recovered(M, nq, rows):
+    # a zero limit makes every wait give up at once: the call returns, says so, and a zero-filled
+    # workspace works again
+    lens = [3000, 500]
+    k, v, table, n, start = ref.make_cache(lens, rows, 2, 64, 0)
+    q = queries(sum(rows), nq, 1)
+    ws = M.paged_workspace(M.PagedKV(k, v, table, n), 8, nq)
+    torch.cuda.synchronize()
+    try:
+        M.moe_debug_set_wait_limit_ns(0)
+        run(M, k, v, table, n, start, q, nq, 8, ws=ws)
+        torch.cuda.synchronize()
+    finally:
+        M.moe_debug_set_wait_limit_ns(2_000_000_000)
+    assert M.moe_workspace_error(ws) == M.MOE_ERR_DEVICE_TIMEOUT
+    ws.zero_()
+    o, lse, _ = run(M, k, v, table, n, start, q, nq, 8, ws=ws)
+    assert M.moe_workspace_error(ws) == 0
+    ref.check_attention(o, lse, ref.attention(q, k, v, table, lens, rows, nq))
