@@ -325,7 +325,7 @@ cudaError_t launch_synthetic_drafts(const int32_t* target, const uint8_t* coin, 
 
 // ------------------------------------------------------------------ serving (paged.cu, logits.cu, serve_capi.cu)
 constexpr int kPagedMaxSeqs = 1024;
-constexpr int kPagedMaxCtas = 320;  // CTAs of the paged attention (partials and join counters are per CTA)
+constexpr int kPagedMaxCtas = 320;  // CTAs of the paged attention (parts of cut units are per CTA)
 
 // A paged cache and the rows of a call (see moe_paged_kv in the header).
 struct PagedRows {
@@ -361,12 +361,17 @@ struct PagedAttnArgs {
   const float* slopes;
   const int32_t *first, *prefix;
 };
+// A CTA's part of a cut (sequence, KV head) unit: part `CTA - cf` of np (0: none).
+struct PagedPart {
+  int cf, np, q0, n, kvh;
+};
+
 // The kernel's arguments: the pages as bf16 tensor maps over [n_pages * nkv *
 // page_size rows][128 dims] (encode_page_map).
 struct PagedAttnParams {
   PagedAttnArgs a;
   CUtensorMap km, vm;
-  unsigned* count;  // [kPagedMaxCtas] parts of a cut unit that arrived, zero between calls
+  PagedPart* rec;   // [kPagedMaxCtas][2] what the parts are of
   float* part_o;    // [kPagedMaxCtas][2][padded rows][128]
   float* part_ml;   // [kPagedMaxCtas][2][padded rows][2]
   uint64_t wait_ns;

@@ -11,11 +11,11 @@ namespace {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// Workspace of the paged calls: the error word first, a join counter per CTA
-// of the attention, then its partials (two segments a CTA, see
-// paged_attn.cu): outputs [rows][128] and (m, l) [rows][2] of the padded rows.
+// Workspace of the paged calls: the error word first, then the attention's
+// parts of cut units (two a CTA, see paged_attn.cu): what they are of, (m, l)
+// [rows][2] and outputs [rows][128] of the padded rows.
 struct PagedLayout {
-  size_t hdr, count, part_o, part_ml, total;
+  size_t hdr, rec, part_o, part_ml, total;
 };
 
 int padded_rows(int n) { return n <= 16 ? 16 : n <= 32 ? 32 : 64; }
@@ -29,7 +29,7 @@ PagedLayout paged_layout(int rows) {
     return r;
   };
   L.hdr = take(256);
-  L.count = take(sizeof(unsigned) * kPagedMaxCtas);
+  L.rec = take(sizeof(PagedPart) * 2 * kPagedMaxCtas);
   L.part_ml = take(sizeof(float) * 2 * kPagedMaxCtas * 2 * padded_rows(rows));
   L.part_o = take(sizeof(float) * (size_t)kPagedMaxCtas * 2 * padded_rows(rows) * 128);
   L.total = off;
@@ -190,7 +190,7 @@ moe_status moe_paged_attention(const moe_paged_kv* kv, const uint16_t* q, int64_
   a.first = scores->first;
   a.prefix = scores->prefix;
   char* b = static_cast<char*>(ws);
-  A.count = reinterpret_cast<unsigned*>(b + L.count);
+  A.rec = reinterpret_cast<PagedPart*>(b + L.rec);
   A.part_ml = reinterpret_cast<float*>(b + L.part_ml);
   A.part_o = reinterpret_cast<float*>(b + L.part_o);
   A.wait_ns = wait_limit_ns();

@@ -206,7 +206,7 @@ def test_same_bits_again_in_any_workspace(M):
     q = queries(10, 16, 1)
     o, lse, ws = run(M, k, v, table, n, start, q, 16, 4)
     big = M.paged_workspace(M.PagedKV(k, v, table, n), 16, 16)
-    big[512 + 4 * 320:].random_(0, 255)  # partials of another shape
+    big[256:].random_(0, 255)  # whatever other calls left
     for w in (ws, ws, big, big):
         o2, lse2, _ = run(M, k, v, table, n, start, q, 16, 4, ws=w)
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
