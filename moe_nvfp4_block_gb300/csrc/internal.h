@@ -356,8 +356,9 @@ struct PagedAttnArgs {
   int64_t qs, os;
   int nq, group, max_rows;
   int window;
-  float scale;                // of q . k
-  float softcap;              // 0: none
+  float scale_log2;           // of q . k, times log2 e
+  float cap_in, cap_log2;     // 2 log2(e) scale / softcap and softcap log2(e); 0: no cap
+  int plain;                  // neither cap nor slopes
   const float* slopes;
   const int32_t *first, *prefix;
 };

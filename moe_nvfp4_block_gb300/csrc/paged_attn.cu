@@ -7,9 +7,10 @@
 //
 // What bounds it: each visible position's keys and values (512 bytes a KV
 // head) are read once.  The work of a call is the list of all 64-position
-// chunks of all (sequence, KV head) units; CTA c of G (two an SM) takes the
-// chunks [c W / G, (c + 1) W / G) of the W, whatever units they fall in, so
-// that unequal lengths cost no balance (with W < G the first W take one each).  A unit inside one CTA is written out
+// chunks of all (sequence, KV head) units, each unit preceded by kPaUnit
+// slots for what its start and end cost; CTA c of G (two an SM) takes the
+// slots [c W / G, (c + 1) W / G) of the W, whatever units they fall in, so
+// that unequal lengths cost no balance.  A unit inside one CTA is written out
 // there; the parts of a cut unit go to the workspace (at most two a CTA) and
 // are joined, in CTA order, by a second kernel whose CTAs share the rows.
 // (The join by the unit's last CTA to arrive, in the same kernel, reads all
@@ -19,12 +20,17 @@
 // A producer warp walks the chunks: it looks up their pages (a chunk is one
 // half or whole page, or several) and loads keys and values by TMA into a
 // ring of three 32 KB stages, with a description of the chunk beside it.
-// Four warps compute.  The unit's rows (verify rows x heads of the KV head)
-// are MT tiles of 16; a warp has one tile and every (4 / MT)th 16-position
-// slice of a chunk: S = Q K^T and O += P V by mma.sync m16n8k16, with P split
-// into two bf16 parts (P = hi + lo to 2^-17: one bf16 P would add as much
-// error as the output's own rounding; the second product is free while the
-// loads bound the kernel).
+// Eight warps compute.  The unit's rows (verify rows x heads of the KV head)
+// are MT tiles of 16; the 8 / MT warps of a tile share a chunk twice: each
+// takes 8 MT positions of S = Q K^T, they agree on the running maximum, leave
+// P in shared memory, and each takes 16 MT dims of O += P V (mma.sync
+// m16n8k16).  So a warp holds few sums (8 MT registers), 18 warps fit an SM,
+// and a unit ends without adding up outputs: a warp alone is bound by the
+// latency of its instructions, and with the positions split all the way (each
+// warp its own maximum and all 128 dims, four warps of 168 registers) a chunk
+// took 1.9 us and a unit's end 2.5 to 4.5.  P is split into two bf16 parts (P
+// = hi + lo to 2^-17: one bf16 P would add as much error as the output's own
+// rounding; the second product is free while the loads bound the kernel).
 //
 // Hidden positions: a score is replaced by -inf, and as 0 * v is not 0 for
 // an infinite or NaN v, a slice with hidden positions is looked over for such
@@ -37,36 +43,34 @@ namespace moe {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kPaWarps = 4;                      // compute warps
+constexpr int kPaWarps = 8;                      // compute warps
 constexpr int kPaThreads = (kPaWarps + 1) * 32;  // and the producer
 constexpr int kPaChunk = 64;
 constexpr int kPaStages = 3;
 constexpr int kPaHalf = kPaChunk * 256;          // a stage's keys (or values)
 constexpr int kPaStageBytes = 2 * kPaHalf;
-constexpr int kPaPitch = 36;                     // floats a row of the merge buffer (32 dims)
+constexpr int kPaUnit = 1;                       // slots before a unit's chunks
 constexpr uint64_t kPaDrainNs = 2000000000ull;
 
 // A chunk as its stage's readers see it.
 struct PaDesc {
   int q0, n, len, kvh;       // the sequence's first row, rows, committed length; KV head
   int pos0, first, prefix;   // the chunk's first position; the sequence's limits
-  int flags;                 // kPaFirst, kPaLast: of the CTA's segment of the unit
+  int flags;                 // kPaLast: the segment's last chunk; kPaEnd; kPaAny, kPaAll
   int cf, np;                // np > 1: a cut unit, whose first CTA is cf and whose parts are np
   int slot, pad;             // where this CTA's part goes (0 / 1)
 };
-constexpr int kPaFirst = 1, kPaLast = 2;
+constexpr int kPaLast = 1, kPaEnd = 2;  // kPaEnd: no chunk, the CTA is done
+constexpr int kPaAny = 4, kPaAll = 8;   // bit of the first of four 16-position slices: some row sees
+                                        // some of it / every row sees all of it
 
 struct PaTable {
   uint64_t full[kPaStages];
   uint64_t empty[kPaStages];
-  uint64_t seg;  // the compute warps' own barrier
+  uint64_t told[kPaStages];  // the description is written (the data may still be on its way)
   PaDesc desc[kPaStages];
-  long long w_total;
-  int nst;
   int abort;
-  float m[kPaWarps][16];
-  float l[kPaWarps][16];
+  float m[kPaWarps * 16];  // [tile][row][part]: maxima of the parts' scores; at a segment's end their sums
 };
 
 // A sequence of the call: its rows, and the chunks that hold their visible
@@ -132,8 +136,7 @@ __device__ __forceinline__ void pa_ldsm_t(uint32_t addr, uint32_t (&r)[4]) {
                : "r"(addr));
 }
 __device__ __forceinline__ void pa_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -145,18 +148,40 @@ __device__ __forceinline__ uint32_t pa_pack(float lo, float hi) {
 }
 __device__ __forceinline__ float ex2(float x) { return exp2f(x); }
 
+// mbar_wait_bounded, with several tries before the first look at the clock.
+__device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns, const volatile int* abort) {
+  if (limit_ns == 0) return false;
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait_bounded(bar, parity, limit_ns, abort);
+}
+
+// Barrier of a tile's warps that also tells whether one has given up.  A warp
+// that gives up (a wait ran out) takes part once more, with `fail`, and
+// leaves; so does every warp at the end: each instance has all of them.
+template <int THREADS>
+__device__ __forceinline__ bool pa_sync(int tile, bool fail) {
+  uint32_t any;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %3, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(any)
+      : "r"((uint32_t)fail), "n"(THREADS), "r"(tile + 1)
+      : "memory");
+  return any == 0;
+}
+
 }  // namespace
 
 template <int MT>
 __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_constant__ PagedAttnParams A) {
-  constexpr int PG = kPaWarps / MT;  // warps (position groups) of a tile
-  constexpr int NSL = kPaChunk / 16 / PG;  // slices of a chunk for a warp
+  constexpr int PARTS = kPaWarps / MT;  // warps of a tile
   const PagedAttnArgs& a = A.a;
   const PagedRows& P = a.p;
   extern __shared__ __align__(1024) unsigned char smem[];
-  float* s_o = reinterpret_cast<float*>(smem + kPaStages * kPaStageBytes);  // [kPaWarps][16][kPaPitch]
-  PaTable& T = *reinterpret_cast<PaTable*>(s_o + kPaWarps * 16 * kPaPitch);
-  int* s_nch = reinterpret_cast<int*>(&T + 1);  // [n_seqs]
+  unsigned char* s_p = smem + kPaStages * kPaStageBytes;  // P: [tile][hi, lo][16 rows][64 positions] bf16
+  PaTable& T = *reinterpret_cast<PaTable*>(s_p + MT * 4096);
+  PaSeq* plan = reinterpret_cast<PaSeq*>(smem);  // [n_seqs], in the ring before its first load
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x;
   const int lbr = min(P.lps, 6), br = 1 << lbr;  // positions of a box
@@ -166,8 +191,8 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
     for (int i = 0; i < kPaStages; ++i) {
       mbar_init(&T.full[i], 1);
       mbar_init(&T.empty[i], kPaWarps);
+      mbar_init(&T.told[i], 1);
     }
-    mbar_init(&T.seg, kPaWarps);
     fence_mbar_init();
     prefetch_tensormap(&A.km);
     prefetch_tensormap(&A.vm);
@@ -175,19 +200,19 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
   pdl_wait();
   pdl_launch_dependents();
   if (threadIdx.x == 0) A.rec[cta * 2].np = A.rec[cta * 2 + 1].np = 0;  // no parts yet
-  for (int b = threadIdx.x; b < P.n_seqs; b += kPaThreads) s_nch[b] = pa_seq(a, b, cta == 0 ? P.err : nullptr).nch;
+  for (int b = threadIdx.x; b < P.n_seqs; b += kPaThreads) plan[b] = pa_seq(a, b, cta == 0 ? P.err : nullptr);
   __syncthreads();
 
   volatile int* abort = &T.abort;
   if (warp == kPaWarps) {
     // ---------------------------------------------------------------- producer
     // lane l sums the sequences [l k, (l + 1) k); the lane that holds the
-    // CTA's first chunk finds its sequence
+    // CTA's first slot finds its sequence
+    auto slots = [&](int nch) { return nch > 0 ? (long long)P.nkv * (nch + kPaUnit) : 0LL; };
     const int k = (P.n_seqs + 31) / 32;
     long long sum = 0;
     for (int i = 0; i < k; ++i)
-      if (lane * k + i < P.n_seqs) sum += s_nch[lane * k + i];
-    sum *= P.nkv;
+      if (lane * k + i < P.n_seqs) sum += slots(plan[lane * k + i].nch);
     long long inc = sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -195,103 +220,120 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
       if (lane >= d) inc += o;
     }
     const long long W = __shfl_sync(0xffffffffu, inc, 31);
-    // no more CTAs than chunks: every one of a cut unit's CTAs has a part
+    // no more CTAs than slots: every CTA inside a cut unit has a part of it
     const int G = (int)min((long long)gridDim.x, W);
-    const long long w0 = cta < G ? cta * W / G : W, w1 = cta < G ? (cta + 1) * W / G : W;
+    const bool small = W < 1 << 22;  // 32-bit divisions do
+    auto div = [&](long long x, long long y) {
+      return small ? (long long)((unsigned)x / (unsigned)y) : x / y;
+    };
+    const long long w0 = cta < G ? div(cta * W, G) : W, w1 = cta < G ? div((cta + 1) * W, G) : W;
     long long base = inc - sum;
     int b = lane * k;
     const bool mine = base <= w0 && w0 < inc;
     if (mine)
-      while (base + (long long)P.nkv * s_nch[b] <= w0) base += (long long)P.nkv * s_nch[b++];
+      while (base + slots(plan[b].nch) <= w0) base += slots(plan[b++].nch);
     const unsigned who = __ballot_sync(0xffffffffu, mine);
     const int src = who ? __ffs(who) - 1 : 0;
     b = __shfl_sync(0xffffffffu, b, src);
     base = __shfl_sync(0xffffffffu, base, src);
-    if (lane == 0) T.nst = (int)(w1 - w0);
-    __syncthreads();
+    PaSeq s{};
+    if (w0 < w1) s = plan[b];
+    // the plan's memory becomes the ring's: its reads before the async writes
+    __syncwarp();
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 
     const uint64_t pol = policy_evict_first();
-    PaSeq s{};
-    int nch = 0, kvh = 0, j = 0;  // of the current unit; j: the chunk
-    bool fresh = true;
-    int cf = 0, np = 1, slot = 0, st = 0;
-    for (; st < (int)(w1 - w0); ++st) {
-      const long long w = w0 + st;
-      int flags = 0;
-      if (st == 0 || j == nch) {  // a new unit
-        flags = kPaFirst;
-        if (st > 0) {
-          j = 0;
-          if (++kvh == P.nkv) {
-            base += (long long)P.nkv * nch;
-            do ++b;
-            while (s_nch[b] == 0);
-            kvh = 0;
-            fresh = true;
-          }
-        }
-        if (fresh) {
-          s = pa_seq(a, b, nullptr);
-          nch = s_nch[b];
-          fresh = false;
-          if (st == 0) {
-            kvh = (int)((w - base) / nch);
-            j = (int)((w - base) - (long long)kvh * nch);
-          }
-        }
-        const long long us = base + (long long)kvh * nch, ue = us + nch;
-        slot = us >= w0;
-        np = 1;
-        if (us < w0 || ue > w1) {
-          cf = (int)(((us + 1) * G - 1) / W);
-          np = (int)((ue * G - 1) / W) - cf + 1;
-        }
-      }
-      if (j == nch - 1 || st == (int)(w1 - w0) - 1) flags |= kPaLast;
-      const int pos0 = (j < s.np ? s.cp + j : s.cm + j - s.np) * kPaChunk;
-      ++j;
-      // this lane's box of the chunk
-      const int p0 = pos0 + (lane << lbr);
-      bool load = lane < (kPaChunk >> lbr) && pa_any(s.len, s.n, s.first, s.prefix, a.window, p0, p0 + br - 1);
-      int row = 0;
-      if (load) {
-        int page = P.table[(size_t)b * P.max_pages + (p0 >> P.lps)];
-        if (page < 0 || page >= P.n_pages) {
-          atomicCAS(P.err, 0, (int)MOE_ERR_INVALID_ARG);
-          page = 0;
-        }
-        row = ((page * P.nkv + kvh) << P.lps) + (p0 & ((1 << P.lps) - 1));
-      }
-      const unsigned boxes = __ballot_sync(0xffffffffu, load);
+    const int lnb = 6 - lbr;  // log2 of a chunk's boxes
+    int st = 0;
+    // A stage: its description (written by lane 0) and its bytes; false: given up.
+    auto begin = [&]() {
       const int sl = st % kPaStages;
       bool ok = true;
       if (st >= kPaStages)
-        ok = !*abort && mbar_wait_bounded(&T.empty[sl], (uint32_t)(st / kPaStages - 1) & 1u, A.wait_ns, abort);
-      if (!__all_sync(0xffffffffu, ok)) {
-        *abort = 1;
-        break;
+        ok = !*abort && pa_wait(&T.empty[sl], (uint32_t)(st / kPaStages - 1) & 1u, A.wait_ns, abort);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) *abort = 1;
+      return ok;
+    };
+    bool live = true;
+    int kvh = s.nch > 0 ? (int)div(w0 - base, s.nch + kPaUnit) : 0;
+    // page cache: lane l holds box l & (boxes - 1) of chunk cj + (l >> lnb) of sequence cb
+    int cb = -1, cj = 0, crow = 0;
+    bool cload = false;
+    while (live) {
+      const int span = s.nch + kPaUnit;
+      const long long rs = base + (long long)kvh * span + kPaUnit, re = rs + s.nch;  // the unit's chunks
+      if (rs >= w1 || w0 >= w1) break;
+      const int j0 = rs >= w0 ? 0 : (int)(w0 - rs), j1 = (int)(min(re, w1) - rs);
+      int cf = 0, np = 1;
+      if (rs < w0 || re > w1) {
+        cf = (int)div((rs + 1) * G - 1, W);
+        np = (int)div(re * G - 1, W) - cf + 1;
       }
+      for (int j = j0; j < j1; ++j) {
+        if (b != cb || j < cj || j >= cj + (32 >> lnb)) {
+          cb = b;
+          cj = j;
+          const int c = j + (lane >> lnb);
+          const int p0 = (c < s.np ? s.cp + c : s.cm + c - s.np) * kPaChunk + ((lane & ((1 << lnb) - 1)) << lbr);
+          cload = c < s.nch && pa_any(s.len, s.n, s.first, s.prefix, a.window, p0, p0 + br - 1);
+          if (cload) {
+            int page = P.table[(size_t)b * P.max_pages + (p0 >> P.lps)];
+            if (page < 0 || page >= P.n_pages) {
+              atomicCAS(P.err, 0, (int)MOE_ERR_INVALID_ARG);
+              page = 0;
+            }
+            crow = (page * P.nkv << P.lps) + (p0 & ((1 << P.lps) - 1));
+          }
+        }
+        live = begin();
+        if (!live) break;
+        const bool load = cload && (lane >> lnb) == j - cj;
+        const unsigned boxes = __ballot_sync(0xffffffffu, load);
+        const int pos0 = (j < s.np ? s.cp + j : s.cm + j - s.np) * kPaChunk, sp = pos0 + 16 * (lane & 3);
+        const unsigned any = __ballot_sync(0xffffffffu, pa_any(s.len, s.n, s.first, s.prefix, a.window, sp, sp + 15));
+        const unsigned all = __ballot_sync(0xffffffffu, pa_all(s.len, s.n, s.first, s.prefix, a.window, sp, sp + 15));
+        const int sl = st % kPaStages;
+        if (lane == 0) {
+          PaDesc& d = T.desc[sl];
+          d.q0 = s.q0;
+          d.n = s.n;
+          d.len = s.len;
+          d.kvh = kvh;
+          d.pos0 = pos0;
+          d.first = s.first;
+          d.prefix = s.prefix;
+          d.flags = (j == j1 - 1 ? kPaLast : 0) | (int)(any & 15u) << kPaAny | (int)(all & 15u) << kPaAll;
+          d.cf = cf;
+          d.np = np;
+          d.slot = rs >= w0;
+          mbar_arrive(&T.told[sl]);
+          mbar_arrive_expect_tx(&T.full[sl], __popc(boxes) * (uint32_t)(br * 512));
+        }
+        __syncwarp();
+        if (load) {
+          unsigned char* dst = smem + (size_t)sl * kPaStageBytes + (lane & ((1 << lnb) - 1)) * (br * 256);
+          const int row = crow + (kvh << P.lps);
+          tma_load_3d(dst, &A.km, 0, row, 0, &T.full[sl], pol);
+          tma_load_3d(dst + kPaHalf, &A.vm, 0, row, 0, &T.full[sl], pol);
+        }
+        ++st;
+      }
+      if (!live || re >= w1) break;
+      if (++kvh == P.nkv) {
+        base += (long long)P.nkv * span;
+        kvh = 0;
+        do s = pa_seq(a, ++b, nullptr);
+        while (s.nch == 0);
+      }
+    }
+    if (live && (live = begin())) {
       if (lane == 0) {
-        PaDesc& d = T.desc[sl];
-        d.q0 = s.q0;
-        d.n = s.n;
-        d.len = s.len;
-        d.kvh = kvh;
-        d.pos0 = pos0;
-        d.first = s.first;
-        d.prefix = s.prefix;
-        d.flags = flags;
-        d.cf = cf;
-        d.np = np;
-        d.slot = slot;
-        mbar_arrive_expect_tx(&T.full[sl], __popc(boxes) * (uint32_t)(br * 512));
+        T.desc[st % kPaStages].flags = kPaEnd;
+        mbar_arrive(&T.told[st % kPaStages]);
+        mbar_arrive(&T.full[st % kPaStages]);
       }
-      __syncwarp();
-      if (load) {
-        unsigned char* dst = smem + (size_t)sl * kPaStageBytes + lane * (br * 256);
-        tma_load_3d(dst, &A.km, 0, row, 0, &T.full[sl], pol);
-        tma_load_3d(dst + kPaHalf, &A.vm, 0, row, 0, &T.full[sl], pol);
-      }
+      ++st;
     }
     __syncwarp();
     __syncthreads();  // every warp is done with the ring
@@ -305,192 +347,204 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
 
   // ------------------------------------------------------------------ compute
   const int g = lane >> 2, t = lane & 3;
-  const int tile = warp % MT, pg = warp / MT;
+  const int tile = warp % MT, part = warp / MT;
   const int lj = lane >> 3, lr = lane & 7;
-  const bool plain = a.softcap == 0.f && !a.slopes;
-  const float scale_log2 = a.scale * kLog2e;
-  const float cap_in = a.softcap > 0.f ? 2.f * kLog2e * a.scale / a.softcap : 0.f;
-  const float cap_log2 = a.softcap * kLog2e;
+  auto sync = [&](bool fail) { return pa_sync<PARTS * 32>(tile, fail); };
+  float* t_m = T.m + tile * 16 * PARTS;
+  const uint32_t p_hi = smem_addr(s_p + tile * 4096);  // lo 2048 bytes on
+  const uint32_t hb = br * 128;                        // bytes of a box's dim half
   uint32_t qa[8][4];
-  float m[2], l[2], o[16][4], slope[2] = {0.f, 0.f};
+  float m[2], l[2], o[2 * MT][4], slope[2] = {0.f, 0.f};
   int rp[2] = {0, 0};  // positions of this thread's two rows
-  // Barrier of the compute warps.  Bounded, and left when a warp has given
-  // up (a plain barrier would wait for that warp for ever): false then.
-  uint32_t seg_parity = 0;
-  auto pa_sync = [&]() {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&T.seg);
-    const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(&T.seg, seg_parity, A.wait_ns, abort));
-    seg_parity ^= 1u;
-    if (!ok) *abort = 1;
-    return ok;
-  };
-  __syncthreads();
-  const int nst = T.nst;
+  bool fresh = true;  // a segment begins
 
-  for (int st = 0; st < nst; ++st) {
+  for (int st = 0;; ++st) {
     const int sl = st % kPaStages;
-    bool ok = !*abort && mbar_wait_bounded(&T.full[sl], (uint32_t)(st / kPaStages) & 1u, A.wait_ns, abort);
-    if (!__all_sync(0xffffffffu, ok)) {
-      *abort = 1;
-      break;
-    }
-    const PaDesc d = T.desc[sl];
-    const int nrow = d.n * a.group;
-    if (d.flags & kPaFirst) {
-#pragma unroll
-      for (int hr = 0; hr < 2; ++hr) {
-        const int i = 16 * tile + g + 8 * hr;
-        const uint32_t* q = nullptr;
-        rp[hr] = d.len;
-        if (i < nrow) {
-          const int r = i / a.group, h = d.kvh * a.group + i - r * a.group;
-          q = reinterpret_cast<const uint32_t*>(a.q + (d.q0 + r) * a.qs + h * 128);
-          rp[hr] = d.len + r;
-          if (a.slopes) slope[hr] = a.slopes[h] * kLog2e;
-        }
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          qa[ks][hr] = q ? q[8 * ks + t] : 0u;
-          qa[ks][2 + hr] = q ? q[8 * ks + 4 + t] : 0u;
-        }
-        m[hr] = -INFINITY;
-        l[hr] = 0.f;
-      }
-#pragma unroll
-      for (int nb = 0; nb < 16; ++nb)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) o[nb][c] = 0.f;
-    }
-    const uint32_t stage = smem_addr(smem + (size_t)sl * kPaStageBytes);
-    if (16 * tile < nrow) {
-      for (int is = 0; is < NSL; ++is) {
-        const int row0 = 16 * (pg + PG * is), pb = d.pos0 + row0;
-        if (!pa_any(d.len, d.n, d.first, d.prefix, a.window, pb, pb + 15)) continue;
-        const bool clear = pa_all(d.len, d.n, d.first, d.prefix, a.window, pb, pb + 15);
-        const uint32_t kbase = stage + ((row0 >> lbr) << (lbr + 8)) + (row0 & (br - 1)) * 128;
-        const uint32_t vbase = kbase + kPaHalf, hb = br * 128;  // hb: bytes of a box's dim half
-        float sc[2][4];
-#pragma unroll
-        for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) sc[nb][c] = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          // matrices: (positions 0-7 | 8-15) x (dims lo | hi of the k-step)
-          uint32_t kb[4];
-          const int rr = 8 * (lj >> 1) + lr, c = (2 * ks + (lj & 1)) & 7;
-          pa_ldsm(kbase + (ks >> 2) * hb + rr * 128 + ((c ^ lr) << 4), kb);
-          pa_mma(sc[0], qa[ks], kb[0], kb[1]);
-          pa_mma(sc[1], qa[ks], kb[2], kb[3]);
-        }
-        // scores in the log2 domain: (row g + 8 (c >> 1), position 8 nb + 2t + (c & 1))
-        if (plain) {
-#pragma unroll
-          for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) sc[nb][c] *= scale_log2;
-        } else {
-#pragma unroll
-          for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              // tanh(z) = 1 - 2 / (e^2z + 1): off by an FP32 rounding of 1,
-              // an absolute error, which is what a score needs
-              float x = sc[nb][c] * scale_log2;
-              if (a.softcap > 0.f) x = cap_log2 * (1.f - __fdividef(2.f, ex2(sc[nb][c] * cap_in) + 1.f));
-              sc[nb][c] = x + slope[c >> 1] * (float)(pb + 8 * nb + 2 * t + (c & 1) - rp[c >> 1]);
-            }
-        }
-        auto seen = [&](int hr, int p) {
-          return p <= rp[hr] && p >= d.first && (a.window == 0 || p > rp[hr] - a.window || p < d.prefix);
-        };
-        if (!clear) {
-#pragma unroll
-          for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              if (!seen(c >> 1, pb + 8 * nb + 2 * t + (c & 1))) sc[nb][c] = -INFINITY;
-        }
-        float al[2];
+    const uint32_t par = (uint32_t)(st / kPaStages) & 1u;
+    const PaDesc& D = T.desc[sl];
+    bool ok = !*abort;
+    if (fresh) {  // the rows are loaded while the keys are on their way
+      ok = ok && pa_wait(&T.told[sl], par, A.wait_ns, abort);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok && !(D.flags & kPaEnd)) {
 #pragma unroll
         for (int hr = 0; hr < 2; ++hr) {
-          float v = fmaxf(fmaxf(sc[0][2 * hr], sc[0][2 * hr + 1]), fmaxf(sc[1][2 * hr], sc[1][2 * hr + 1]));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-          const float mx = fmaxf(m[hr], v);
-          const float ref = mx == -INFINITY ? 0.f : mx;  // nothing visible yet
-          al[hr] = ex2(m[hr] - ref);
-          m[hr] = mx;
-          float add = 0.f;
+          const int i = 16 * tile + g + 8 * hr;
+          const uint32_t* q = nullptr;
+          rp[hr] = D.len;
+          if (i < D.n * a.group) {
+            const int r = i / a.group, h = D.kvh * a.group + i - r * a.group;
+            q = reinterpret_cast<const uint32_t*>(a.q + (D.q0 + r) * a.qs + h * 128);
+            rp[hr] += r;
+            if (a.slopes) slope[hr] = a.slopes[h] * 1.4426950408889634f;
+          }
 #pragma unroll
-          for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              sc[nb][2 * hr + c] = ex2(sc[nb][2 * hr + c] - ref);
-              add += sc[nb][2 * hr + c];
-            }
-          l[hr] = l[hr] * al[hr] + add;
+          for (int ks = 0; ks < 8; ++ks) {
+            qa[ks][hr] = q ? q[8 * ks + t] : 0u;
+            qa[ks][2 + hr] = q ? q[8 * ks + 4 + t] : 0u;
+          }
+          m[hr] = -INFINITY;
+          l[hr] = 0.f;
         }
-        if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
 #pragma unroll
-          for (int nb = 0; nb < 16; ++nb) {
-            o[nb][0] *= al[0];
-            o[nb][1] *= al[0];
-            o[nb][2] *= al[1];
-            o[nb][3] *= al[1];
+        for (int nb = 0; nb < 2 * MT; ++nb)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[nb][c] = 0.f;
+      }
+    }
+    ok = ok && pa_wait(&T.full[sl], par, A.wait_ns, abort);
+    if (!__all_sync(0xffffffffu, ok)) {
+      *abort = 1;
+      sync(true);
+      break;
+    }
+    const int flags = D.flags, pos0 = D.pos0;
+    fresh = (flags & kPaLast) != 0;
+    if (flags & kPaEnd) {
+      sync(false);
+      break;
+    }
+    const int nrow = D.n * a.group;
+    const bool live = 16 * tile < nrow;  // the tile has rows
+    if (live) {
+      const uint32_t stage = smem_addr(smem + (size_t)sl * kPaStageBytes);
+      auto row_at = [&](int r) { return stage + ((r >> lbr) << (lbr + 8)) + (r & (br - 1)) * 128; };
+      auto seen = [&](int hr, int p) {
+        return p <= rp[hr] && p >= D.first && (a.window == 0 || p > rp[hr] - a.window || p < D.prefix);
+      };
+      // S: this warp's 8 MT positions
+      float sc[MT][4];
+#pragma unroll
+      for (int nb = 0; nb < MT; ++nb) {
+        float sd[4] = {0.f, 0.f, 0.f, 0.f};  // odd k-steps: a chain of their own
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sc[nb][c] = 0.f;
+        const uint32_t kb = row_at(8 * (MT * part + nb)) + lr * 128;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t f[4];  // dims 32 q + 0-7, 8-15, 16-23, 24-31
+          pa_ldsm(kb + (q >> 1) * hb + (((4 * (q & 1) + lj) ^ lr) << 4), f);
+          pa_mma(sc[nb], qa[2 * q], f[0], f[1]);
+          pa_mma(sd, qa[2 * q + 1], f[2], f[3]);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sc[nb][c] += sd[c];
+      }
+      // scores in the log2 domain: (row g + 8 (c >> 1), position 8 nb + 2t + (c & 1))
+#pragma unroll
+      for (int nb = 0; nb < MT; ++nb) {
+        const int w = 8 * (MT * part + nb), pb = pos0 + w;
+        if (a.plain) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) sc[nb][c] *= a.scale_log2;
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            // tanh(z) = 1 - 2 / (e^2z + 1): off by an FP32 rounding of 1, an
+            // absolute error, which is what a score needs
+            float x = sc[nb][c] * a.scale_log2;
+            if (a.cap_log2 > 0.f) x = a.cap_log2 * (1.f - __fdividef(2.f, ex2(sc[nb][c] * a.cap_in) + 1.f));
+            sc[nb][c] = x + slope[c >> 1] * (float)(pb + 2 * t + (c & 1) - rp[c >> 1]);
           }
         }
-        // V by transposing ldmatrix: (positions 0-7 | 8-15) x (dims 16 np + 0-7 | 8-15)
-        auto load_v = [&](int np, uint32_t(&vb)[4]) {
-          const int rr = 8 * (lj & 1) + lr, c = (2 * np + (lj >> 1)) & 7;
-          pa_ldsm_t(vbase + (np >> 2) * hb + rr * 128 + ((c ^ lr) << 4), vb);
-        };
+        if (!(flags >> (kPaAll + (w >> 4)) & 1)) {
+          const bool some = flags >> (kPaAny + (w >> 4)) & 1;  // else its page may not even be loaded
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (!some || !seen(c >> 1, pb + 2 * t + (c & 1))) sc[nb][c] = -INFINITY;
+        }
+      }
+#pragma unroll
+      for (int hr = 0; hr < 2; ++hr) {
+        float v = -INFINITY;
+#pragma unroll
+        for (int nb = 0; nb < MT; ++nb) v = fmaxf(v, fmaxf(sc[nb][2 * hr], sc[nb][2 * hr + 1]));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+        if (t == 0) t_m[(g + 8 * hr) * PARTS + part] = v;
+      }
+      if (!sync(false)) break;
+      float al[2];
+#pragma unroll
+      for (int hr = 0; hr < 2; ++hr) {
+        float mx = m[hr];
+#pragma unroll
+        for (int w = 0; w < PARTS; ++w) mx = fmaxf(mx, t_m[(g + 8 * hr) * PARTS + w]);
+        const float ref = mx == -INFINITY ? 0.f : mx;  // nothing visible yet
+        al[hr] = ex2(m[hr] - ref);
+        m[hr] = mx;
+        l[hr] *= al[hr];
+#pragma unroll
+        for (int nb = 0; nb < MT; ++nb) {
+          const float x = ex2(sc[nb][2 * hr] - ref), y = ex2(sc[nb][2 * hr + 1] - ref);
+          l[hr] += x + y;
+          const uint32_t hi = pa_pack(x, y);
+          const uint32_t lo = pa_pack(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u));
+          const uint32_t at = p_hi + (g + 8 * hr) * 128 + (((MT * part + nb) ^ g) << 4) + 4 * t;
+          asm volatile("st.shared.u32 [%0], %1;\n st.shared.u32 [%0 + 2048], %2;" ::"r"(at), "r"(hi), "r"(lo) : "memory");
+        }
+      }
+      if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
+#pragma unroll
+        for (int nb = 0; nb < 2 * MT; ++nb) {
+          o[nb][0] *= al[0];
+          o[nb][1] *= al[0];
+          o[nb][2] *= al[1];
+          o[nb][3] *= al[1];
+        }
+      }
+      if (!sync(false)) break;
+      // O: this warp's 16 MT dims over the chunk's positions
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        if (!(flags >> (kPaAny + ks) & 1)) continue;
+        uint32_t ph[4], pl[4];
+        const uint32_t at = p_hi + (lr + 8 * (lj & 1)) * 128 + (((2 * ks + (lj >> 1)) ^ lr) << 4);
+        pa_ldsm(at, ph);
+        pa_ldsm(at + 2048, pl);
+        const uint32_t vrow = row_at(16 * ks) + kPaHalf;
+        uint32_t vb[MT][4];  // (positions 0-7 | 8-15) x (dims 0-7 | 8-15) of each 16 dims
         bool odd = false;
-        if (!clear) {
 #pragma unroll
-          for (int np = 0; np < 8; ++np) {
-            uint32_t vb[4];
-            load_v(np, vb);
+        for (int n = 0; n < MT; ++n) {
+          const int c = 2 * (MT * part + n) + (lj >> 1);
+          pa_ldsm_t(vrow + (c >> 3) * hb + (8 * (lj & 1) + lr) * 128 + (((c & 7) ^ lr) << 4), vb[n]);
+        }
+        if (!(flags >> (kPaAll + ks) & 1)) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) odd |= __vcmpeq2(vb[u] & 0x7F807F80u, 0x7F807F80u) != 0u;
-          }
+          for (int n = 0; n < MT; ++n)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) odd |= __vcmpeq2(vb[n][u] & 0x7F807F80u, 0x7F807F80u) != 0u;
           odd = __any_sync(0xffffffffu, odd);
         }
         if (!odd) {
-          uint32_t ph[4], pl[4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float x = sc[u >> 1][2 * (u & 1)], y = sc[u >> 1][2 * (u & 1) + 1];
-            ph[u] = pa_pack(x, y);
-            pl[u] = pa_pack(x - __uint_as_float(ph[u] << 16), y - __uint_as_float(ph[u] & 0xFFFF0000u));
-          }
-#pragma unroll
-          for (int np = 0; np < 8; ++np) {
-            uint32_t vb[4];
-            load_v(np, vb);
-            pa_mma(o[2 * np], ph, vb[0], vb[1]);
-            pa_mma(o[2 * np + 1], ph, vb[2], vb[3]);
-            pa_mma(o[2 * np], pl, vb[0], vb[1]);
-            pa_mma(o[2 * np + 1], pl, vb[2], vb[3]);
+          for (int n = 0; n < MT; ++n) {
+            pa_mma(o[2 * n], ph, vb[n][0], vb[n][1]);
+            pa_mma(o[2 * n + 1], ph, vb[n][2], vb[n][3]);
+            pa_mma(o[2 * n], pl, vb[n][0], vb[n][1]);
+            pa_mma(o[2 * n + 1], pl, vb[n][2], vb[n][3]);
           }
         } else {
           // element by element over the visible positions
+#pragma unroll 1
           for (int pp = 0; pp < 16; ++pp) {
-            const int from = (lane & ~3) | ((pp & 7) >> 1);
             float p[2];
 #pragma unroll
             for (int hr = 0; hr < 2; ++hr) {
-              const float x0 = pp < 8 ? sc[0][2 * hr] : sc[1][2 * hr], x1 = pp < 8 ? sc[0][2 * hr + 1] : sc[1][2 * hr + 1];
-              p[hr] = __shfl_sync(0xffffffffu, (pp & 1) ? x1 : x0, from);
+              uint16_t hi, lo;
+              const uint32_t e = p_hi + (g + 8 * hr) * 128 + (((2 * ks + (pp >> 3)) ^ g) << 4) + 2 * (pp & 7);
+              asm volatile("ld.shared.u16 %0, [%2];\n ld.shared.u16 %1, [%2 + 2048];" : "=h"(hi), "=h"(lo) : "r"(e));
+              p[hr] = bf16_bits_to_float(hi) + bf16_bits_to_float(lo);
             }
-            const bool see0 = seen(0, pb + pp), see1 = seen(1, pb + pp);
+            const bool see0 = seen(0, pos0 + 16 * ks + pp), see1 = seen(1, pos0 + 16 * ks + pp);
 #pragma unroll
-            for (int nb = 0; nb < 16; ++nb) {
+            for (int nb = 0; nb < 2 * MT; ++nb) {
+              const int c = 2 * MT * part + nb;
               uint32_t v;
               asm volatile("ld.shared.u32 %0, [%1];"
                            : "=r"(v)
-                           : "r"(vbase + (nb >> 3) * hb + pp * 128 + (((nb & 7) ^ (pp & 7)) << 4) + 4 * t));
+                           : "r"(vrow + (c >> 3) * hb + pp * 128 + (((c & 7) ^ (pp & 7)) << 4) + 4 * t));
               const float v0 = __uint_as_float(v << 16), v1 = __uint_as_float(v & 0xFFFF0000u);
               if (see0) {
                 o[nb][0] += p[0] * v0;
@@ -505,84 +559,52 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
         }
       }
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&T.empty[sl]);
-    if (!(d.flags & kPaLast)) continue;
+    if (!(flags & kPaLast)) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&T.empty[sl]);
+      continue;
+    }
 
-    // ---------------------------------------------------------------- the segment's end
-    // The position groups of a tile agree on a maximum; each scales its sums
-    // to it, and they are added in group order, 32 dims at a time.
+    // the segment's end: the row's sum over its parts, then the output or this CTA's part of it
+    if (live) {
 #pragma unroll
-    for (int hr = 0; hr < 2; ++hr) {
-      l[hr] += __shfl_xor_sync(0xffffffffu, l[hr], 1);
-      l[hr] += __shfl_xor_sync(0xffffffffu, l[hr], 2);
-      if (t == 0) {
-        T.m[warp][g + 8 * hr] = m[hr];
-        T.l[warp][g + 8 * hr] = l[hr];
+      for (int hr = 0; hr < 2; ++hr) {
+        l[hr] += __shfl_xor_sync(0xffffffffu, l[hr], 1);
+        l[hr] += __shfl_xor_sync(0xffffffffu, l[hr], 2);
+        if (t == 0) t_m[(g + 8 * hr) * PARTS + part] = l[hr];
       }
-    }
-    if (!pa_sync()) break;
-    float f[2];
+      if (!sync(false)) break;
+      float sum[2] = {0.f, 0.f};
 #pragma unroll
-    for (int hr = 0; hr < 2; ++hr) {
-      float M = -INFINITY;
+      for (int hr = 0; hr < 2; ++hr)
 #pragma unroll
-      for (int w = 0; w < PG; ++w) M = fmaxf(M, T.m[tile + MT * w][g + 8 * hr]);
-      f[hr] = m[hr] == -INFINITY ? 0.f : ex2(m[hr] - M);
-    }
-    const bool whole = d.np == 1;
-    float* po = A.part_o + (size_t)(cta * 2 + d.slot) * (16 * MT * 128);
-    float* pml = A.part_ml + (size_t)(cta * 2 + d.slot) * (16 * MT * 2);
-    const int col = (threadIdx.x & 7) * 4, mr = threadIdx.x >> 3;  // this thread's 4 dims and row of a tile
-    bool live = true;
+        for (int w = 0; w < PARTS; ++w) sum[hr] += t_m[(g + 8 * hr) * PARTS + w];
+      if (!sync(false)) break;  // the next chunk's maxima may come
 #pragma unroll
-    for (int dq = 0; dq < 4; ++dq) {
+      for (int hr = 0; hr < 2; ++hr) {
+        const int i = 16 * tile + g + 8 * hr;
+        if (i >= nrow) continue;
+        const float L = sum[hr];
+        if (D.np == 1) {
+          const int r = i / a.group, h = D.kvh * a.group + i - r * a.group;
+          const float inv = L == 0.f ? 0.f : 1.f / L;
+          uint32_t* out = reinterpret_cast<uint32_t*>(a.o + (D.q0 + r) * a.os + h * 128 + 16 * MT * part);
 #pragma unroll
-      for (int nb = 0; nb < 4; ++nb) {
-        float* r0 = s_o + (warp * 16 + g) * kPaPitch + 8 * nb + 2 * t;
-        *reinterpret_cast<float2*>(r0) = make_float2(o[4 * dq + nb][0] * f[0], o[4 * dq + nb][1] * f[0]);
-        *reinterpret_cast<float2*>(r0 + 8 * kPaPitch) = make_float2(o[4 * dq + nb][2] * f[1], o[4 * dq + nb][3] * f[1]);
-      }
-      live = pa_sync();
-      if (!live) break;
+          for (int nb = 0; nb < 2 * MT; ++nb) out[4 * nb + t] = pa_pack(o[nb][2 * hr] * inv, o[nb][2 * hr + 1] * inv);
+          if (a.lse && t == 0 && part == 0)
+            a.lse[(size_t)(D.q0 + r) * a.nq + h] = L == 0.f ? -INFINITY : (m[hr] + log2f(L)) * 0.6931471805599453f;
+        } else {
+          const size_t row = (size_t)(cta * 2 + D.slot) * (16 * MT) + i;
+          float2* po = reinterpret_cast<float2*>(A.part_o + row * 128 + 16 * MT * part);
 #pragma unroll
-      for (int u = 0; u < MT; ++u) {
-        const int i = 16 * u + mr;
-        if (i < nrow) {
-          float M = -INFINITY, L = 0.f;
-#pragma unroll
-          for (int w = 0; w < PG; ++w) M = fmaxf(M, T.m[u + MT * w][mr]);
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int w = 0; w < PG; ++w) {
-            const float mw = T.m[u + MT * w][mr];
-            L += mw == -INFINITY ? 0.f : T.l[u + MT * w][mr] * ex2(mw - M);
-            const float4 x = *reinterpret_cast<const float4*>(s_o + ((u + MT * w) * 16 + mr) * kPaPitch + col);
-            v.x += x.x;
-            v.y += x.y;
-            v.z += x.z;
-            v.w += x.w;
-          }
-          if (whole) {
-            const int r = i / a.group, h = d.kvh * a.group + i - r * a.group;
-            const float inv = L == 0.f ? 0.f : 1.f / L;
-            *reinterpret_cast<uint2*>(a.o + (d.q0 + r) * a.os + h * 128 + 32 * dq + col) =
-                make_uint2(pa_pack(v.x * inv, v.y * inv), pa_pack(v.z * inv, v.w * inv));
-            if (a.lse && dq == 0 && col == 0)
-              a.lse[(size_t)(d.q0 + r) * a.nq + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-          } else {
-            __stcg(reinterpret_cast<float4*>(po + i * 128 + 32 * dq + col), v);
-            if (dq == 0 && col == 0) __stcg(reinterpret_cast<float2*>(pml + 2 * i), make_float2(M, L));
-          }
+          for (int nb = 0; nb < 2 * MT; ++nb) __stcg(po + 4 * nb + t, make_float2(o[nb][2 * hr], o[nb][2 * hr + 1]));
+          if (t == 0 && part == 0) __stcg(reinterpret_cast<float2*>(A.part_ml + 2 * row), make_float2(m[hr], L));
         }
       }
-      live = pa_sync();
-      if (!live) break;
     }
-    if (!live) break;
-    if (whole) continue;
-
-    if (threadIdx.x == 0) A.rec[cta * 2 + d.slot] = {d.cf, d.np, d.q0, d.n, d.kvh};
+    if (D.np > 1 && threadIdx.x == 0) A.rec[cta * 2 + D.slot] = {D.cf, D.np, D.q0, D.n, D.kvh};
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&T.empty[sl]);
   }
   __syncthreads();  // the ring is free
 }
@@ -673,8 +695,11 @@ cudaError_t launch_paged_attention(const PagedAttnParams& A, cudaStream_t s) {
   const int want = 2 * num_sms();
   cfg.gridDim = dim3(want < kPagedMaxCtas ? want : kPagedMaxCtas);
   cfg.blockDim = dim3(kPaThreads);
-  cfg.dynamicSmemBytes = kPaStages * kPaStageBytes + sizeof(float) * kPaWarps * 16 * kPaPitch + sizeof(PaTable) +
-                         sizeof(int) * A.a.p.n_seqs;
+  const int rows = A.a.max_rows * A.a.group, MT = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  const size_t smem = kPaStages * kPaStageBytes + MT * 4096 + sizeof(PaTable);
+  static_assert(2 * (kPaStages * kPaStageBytes + 4 * 4096 + sizeof(PaTable) + 1024) <= 228 * 1024, "two CTAs an SM");
+  static_assert(sizeof(PaSeq) * kPagedMaxSeqs <= kPaStages * kPaStageBytes, "the plan fits the ring");
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -682,17 +707,16 @@ cudaError_t launch_paged_attention(const PagedAttnParams& A, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   auto run = [&](auto kern) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 114 * 1024);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess) e = max_carveout(kern);
     return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, kern, A) : e;
   };
-  const int rows = A.a.max_rows * A.a.group;
-  const cudaError_t e = rows <= 16 ? run(k_paged_attn<1>) : rows <= 32 ? run(k_paged_attn<2>) : run(k_paged_attn<4>);
+  const cudaError_t e = MT == 1 ? run(k_paged_attn<1>) : MT == 2 ? run(k_paged_attn<2>) : run(k_paged_attn<4>);
   if (e != cudaSuccess) return e;
   cfg.blockDim = dim3(128);
   cfg.dynamicSmemBytes = 0;
   max_carveout(k_paged_join);
-  return cudaLaunchKernelEx(&cfg, k_paged_join, A, rows <= 16 ? 16 : rows <= 32 ? 32 : 64);
+  return cudaLaunchKernelEx(&cfg, k_paged_join, A, 16 * MT);
 }
 
 }  // namespace moe

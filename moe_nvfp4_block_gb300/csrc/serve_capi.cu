@@ -184,8 +184,11 @@ moe_status moe_paged_attention(const moe_paged_kv* kv, const uint16_t* q, int64_
   a.group = nq / kv->nkv;
   a.max_rows = max_rows;
   a.window = scores->window;
-  a.scale = scores->scale > 0.f ? scores->scale : (float)(1.0 / std::sqrt(128.0));
-  a.softcap = scores->softcap;
+  const double log2e = 1.4426950408889634, scale = scores->scale > 0.f ? scores->scale : 1.0 / std::sqrt(128.0);
+  a.scale_log2 = (float)(scale * log2e);
+  a.cap_in = scores->softcap > 0.f ? (float)(2.0 * log2e * scale / scores->softcap) : 0.f;
+  a.cap_log2 = (float)(scores->softcap * log2e);
+  a.plain = !(scores->softcap > 0.f) && !scores->slopes;
   a.slopes = scores->slopes;
   a.first = scores->first;
   a.prefix = scores->prefix;
