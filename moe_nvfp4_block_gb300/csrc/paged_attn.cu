@@ -180,7 +180,8 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
   const PagedRows& P = a.p;
   extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* s_p = smem + kPaStages * kPaStageBytes;  // P: [tile][hi, lo][16 rows][64 positions] bf16
-  PaTable& T = *reinterpret_cast<PaTable*>(s_p + MT * 4096);
+  constexpr bool QS = MT == 2;  // the rows stay in shared memory ([tile][16 rows][128 dims]), not in registers
+  PaTable& T = *reinterpret_cast<PaTable*>(s_p + MT * 4096 + (QS ? MT * 4096 : 0));
   PaSeq* plan = reinterpret_cast<PaSeq*>(smem);  // [n_seqs], in the ring before its first load
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x;
@@ -353,7 +354,8 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
   float* t_m = T.m + tile * 16 * PARTS;
   const uint32_t p_hi = smem_addr(s_p + tile * 4096);  // lo 2048 bytes on
   const uint32_t hb = br * 128;                        // bytes of a box's dim half
-  uint32_t qa[8][4];
+  const uint32_t q_s = smem_addr(s_p + (MT + tile) * 4096);
+  uint32_t qa[QS ? 1 : 8][4];
   float m[2], l[2], o[2 * MT][4], slope[2] = {0.f, 0.f};
   int rp[2] = {0, 0};  // positions of this thread's two rows
   bool fresh = true;  // a segment begins
@@ -378,10 +380,12 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
             rp[hr] += r;
             if (a.slopes) slope[hr] = a.slopes[h] * 1.4426950408889634f;
           }
+          if constexpr (!QS) {
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks) {
-            qa[ks][hr] = q ? q[8 * ks + t] : 0u;
-            qa[ks][2 + hr] = q ? q[8 * ks + 4 + t] : 0u;
+            for (int ks = 0; ks < 8; ++ks) {
+              qa[ks][hr] = q ? q[8 * ks + t] : 0u;
+              qa[ks][2 + hr] = q ? q[8 * ks + 4 + t] : 0u;
+            }
           }
           m[hr] = -INFINITY;
           l[hr] = 0.f;
@@ -390,6 +394,20 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
         for (int nb = 0; nb < 2 * MT; ++nb)
 #pragma unroll
           for (int c = 0; c < 4; ++c) o[nb][c] = 0.f;
+        if constexpr (QS) {
+          for (int u = part * 32 + lane; u < 256; u += PARTS * 32) {
+            const int row = u >> 4, i = 16 * tile + row;
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (i < D.n * a.group) {
+              const int r = i / a.group, h = D.kvh * a.group + i - r * a.group;
+              v = *reinterpret_cast<const uint4*>(a.q + (D.q0 + r) * a.qs + h * 128 + 8 * (u & 15));
+            }
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(q_s + row * 256 + (((u & 15) ^ (row & 7)) << 4)),
+                         "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                         : "memory");
+          }
+          if (!sync(!ok)) break;
+        }
       }
     }
     ok = ok && pa_wait(&T.full[sl], par, A.wait_ns, abort);
@@ -412,24 +430,37 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
       auto seen = [&](int hr, int p) {
         return p <= rp[hr] && p >= D.first && (a.window == 0 || p > rp[hr] - a.window || p < D.prefix);
       };
-      // S: this warp's 8 MT positions
-      float sc[MT][4];
+      // S: this warp's 8 MT positions (odd k-steps in a chain of their own)
+      float sc[MT][4], sd[MT][4];
 #pragma unroll
-      for (int nb = 0; nb < MT; ++nb) {
-        float sd[4] = {0.f, 0.f, 0.f, 0.f};  // odd k-steps: a chain of their own
+      for (int nb = 0; nb < MT; ++nb)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) sc[nb][c] = 0.f;
-        const uint32_t kb = row_at(8 * (MT * part + nb)) + lr * 128;
+        for (int c = 0; c < 4; ++c) sc[nb][c] = sd[nb][c] = 0.f;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t f[4];  // dims 32 q + 0-7, 8-15, 16-23, 24-31
-          pa_ldsm(kb + (q >> 1) * hb + (((4 * (q & 1) + lj) ^ lr) << 4), f);
-          pa_mma(sc[nb], qa[2 * q], f[0], f[1]);
-          pa_mma(sd, qa[2 * q + 1], f[2], f[3]);
+      for (int q = 0; q < 4; ++q) {
+        if constexpr (QS) {
+          const uint32_t at = q_s + (lr + 8 * (lj & 1)) * 256;
+          pa_ldsm(at + (((4 * q + (lj >> 1)) ^ lr) << 4), qa[0]);
         }
+        uint32_t qb[4];
+        if constexpr (QS) pa_ldsm(q_s + (lr + 8 * (lj & 1)) * 256 + (((4 * q + 2 + (lj >> 1)) ^ lr) << 4), qb);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) sc[nb][c] += sd[c];
+        for (int nb = 0; nb < MT; ++nb) {
+          uint32_t f[4];  // dims 32 q + 0-7, 8-15, 16-23, 24-31
+          pa_ldsm(row_at(8 * (MT * part + nb)) + lr * 128 + (q >> 1) * hb + (((4 * (q & 1) + lj) ^ lr) << 4), f);
+          if constexpr (QS) {
+            pa_mma(sc[nb], qa[0], f[0], f[1]);
+            pa_mma(sd[nb], qb, f[2], f[3]);
+          } else {
+            pa_mma(sc[nb], qa[2 * q], f[0], f[1]);
+            pa_mma(sd[nb], qa[2 * q + 1], f[2], f[3]);
+          }
+        }
       }
+#pragma unroll
+      for (int nb = 0; nb < MT; ++nb)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sc[nb][c] += sd[nb][c];
       // scores in the log2 domain: (row g + 8 (c >> 1), position 8 nb + 2t + (c & 1))
 #pragma unroll
       for (int nb = 0; nb < MT; ++nb) {
@@ -495,6 +526,7 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
       }
       if (!sync(false)) break;
       // O: this warp's 16 MT dims over the chunk's positions
+      int odd_slices = 0;
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
         if (!(flags >> (kPaAny + ks) & 1)) continue;
@@ -517,44 +549,45 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
             for (int u = 0; u < 4; ++u) odd |= __vcmpeq2(vb[n][u] & 0x7F807F80u, 0x7F807F80u) != 0u;
           odd = __any_sync(0xffffffffu, odd);
         }
-        if (!odd) {
+        if (odd) {
+          odd_slices |= 1 << ks;
+          continue;
+        }
 #pragma unroll
-          for (int n = 0; n < MT; ++n) {
-            pa_mma(o[2 * n], ph, vb[n][0], vb[n][1]);
-            pa_mma(o[2 * n + 1], ph, vb[n][2], vb[n][3]);
-            pa_mma(o[2 * n], pl, vb[n][0], vb[n][1]);
-            pa_mma(o[2 * n + 1], pl, vb[n][2], vb[n][3]);
-          }
-        } else {
-          // element by element over the visible positions
+        for (int n = 0; n < MT; ++n) {
+          pa_mma(o[2 * n], ph, vb[n][0], vb[n][1]);
+          pa_mma(o[2 * n + 1], ph, vb[n][2], vb[n][3]);
+          pa_mma(o[2 * n], pl, vb[n][0], vb[n][1]);
+          pa_mma(o[2 * n + 1], pl, vb[n][2], vb[n][3]);
+        }
+      }
+      // slices with infinite or NaN values: element by element over the visible positions
 #pragma unroll 1
-          for (int pp = 0; pp < 16; ++pp) {
-            float p[2];
+      for (int pp = 0; odd_slices && pp < kPaChunk; ++pp) {
+        if (!(odd_slices >> (pp >> 4) & 1)) continue;
+        float p[2];
 #pragma unroll
-            for (int hr = 0; hr < 2; ++hr) {
-              uint16_t hi, lo;
-              const uint32_t e = p_hi + (g + 8 * hr) * 128 + (((2 * ks + (pp >> 3)) ^ g) << 4) + 2 * (pp & 7);
-              asm volatile("ld.shared.u16 %0, [%2];\n ld.shared.u16 %1, [%2 + 2048];" : "=h"(hi), "=h"(lo) : "r"(e));
-              p[hr] = bf16_bits_to_float(hi) + bf16_bits_to_float(lo);
-            }
-            const bool see0 = seen(0, pos0 + 16 * ks + pp), see1 = seen(1, pos0 + 16 * ks + pp);
+        for (int hr = 0; hr < 2; ++hr) {
+          uint16_t hi, lo;
+          const uint32_t e = p_hi + (g + 8 * hr) * 128 + (((pp >> 3) ^ g) << 4) + 2 * (pp & 7);
+          asm volatile("ld.shared.u16 %0, [%2];\n ld.shared.u16 %1, [%2 + 2048];" : "=h"(hi), "=h"(lo) : "r"(e));
+          p[hr] = bf16_bits_to_float(hi) + bf16_bits_to_float(lo);
+        }
+        const bool see0 = seen(0, pos0 + pp), see1 = seen(1, pos0 + pp);
+        const uint32_t vrow = row_at(pp) + kPaHalf + 4 * t;
 #pragma unroll
-            for (int nb = 0; nb < 2 * MT; ++nb) {
-              const int c = 2 * MT * part + nb;
-              uint32_t v;
-              asm volatile("ld.shared.u32 %0, [%1];"
-                           : "=r"(v)
-                           : "r"(vrow + (c >> 3) * hb + pp * 128 + (((c & 7) ^ (pp & 7)) << 4) + 4 * t));
-              const float v0 = __uint_as_float(v << 16), v1 = __uint_as_float(v & 0xFFFF0000u);
-              if (see0) {
-                o[nb][0] += p[0] * v0;
-                o[nb][1] += p[0] * v1;
-              }
-              if (see1) {
-                o[nb][2] += p[1] * v0;
-                o[nb][3] += p[1] * v1;
-              }
-            }
+        for (int nb = 0; nb < 2 * MT; ++nb) {
+          const int c = 2 * MT * part + nb;
+          uint32_t v;
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(vrow + (c >> 3) * hb + (((c & 7) ^ (pp & 7)) << 4)));
+          const float v0 = __uint_as_float(v << 16), v1 = __uint_as_float(v & 0xFFFF0000u);
+          if (see0) {
+            o[nb][0] += p[0] * v0;
+            o[nb][1] += p[0] * v1;
+          }
+          if (see1) {
+            o[nb][2] += p[1] * v0;
+            o[nb][3] += p[1] * v1;
           }
         }
       }
@@ -611,17 +644,22 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
 
 // The join of cut units: CTA c takes its share of the rows of the (at most
 // two) units it had a part of, row i going to part i mod np.  Up to eight
-// parts: a warp per row, every load in flight at once; more: the CTA's warps
-// share a row's parts.  Parts are added in a fixed order.
-__global__ void __launch_bounds__(128) k_paged_join(const __grid_constant__ PagedAttnParams A, int rows) {
-  __shared__ float s_l[4];
-  __shared__ float4 s_v[4][32];
+// parts: a warp per row; more: the CTA's warps share a row's parts.  Either
+// way a row's loads are all in flight at once (for up to 64 parts), and the
+// parts are added in a fixed order.
+constexpr int kPjWarps = 8;
+
+__global__ void __launch_bounds__(kPjWarps * 32) k_paged_join(const __grid_constant__ PagedAttnParams A, int rows) {
+  __shared__ float s_l[kPjWarps];
+  __shared__ float4 s_v[kPjWarps][32];
   const PagedAttnArgs& a = A.a;
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
+  PagedPart both[2] = {A.rec[c * 2], A.rec[c * 2 + 1]};
+#pragma unroll
   for (int slot = 0; slot < 2; ++slot) {
-    const PagedPart R = A.rec[c * 2 + slot];
+    const PagedPart R = both[slot];
     if (R.np < 2) continue;
     const int nrow = R.n * a.group, p = c - R.cf;
     const bool wide = R.np > 8;
@@ -634,15 +672,12 @@ __global__ void __launch_bounds__(128) k_paged_join(const __grid_constant__ Page
       if (a.lse && lane == 0)
         a.lse[(size_t)(R.q0 + r) * a.nq + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
     };
-    for (int i = p + (wide ? 0 : R.np * warp); i < nrow; i += wide ? R.np : 4 * R.np) {
+    for (int i = p + (wide ? 0 : R.np * warp); i < nrow; i += wide ? R.np : kPjWarps * R.np) {
       // this warp's parts of row i: u0, u0 + du, ...
-      const int u0 = wide ? warp : 0, du = wide ? 4 : 1;
-      float M = -INFINITY;
-      for (int u = lane; u < R.np; u += 32) M = fmaxf(M, __ldcg(A.part_ml + 2 * part(u, i)));
+      const int u0 = wide ? warp : 0, du = wide ? kPjWarps : 1;
+      float M = -INFINITY, L = 0.f;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      float L = 0.f;
-      bool first = true;
-      for (int b = u0; b < R.np; b += 8 * du) {
+      for (int b = u0; b < R.np || b == u0; b += 8 * du) {
         float4 x[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k)
@@ -651,10 +686,10 @@ __global__ void __launch_bounds__(128) k_paged_join(const __grid_constant__ Page
         float2 ml = make_float2(-INFINITY, 0.f);
         if (lane < 8 && b + lane * du < R.np)
           ml = __ldcg(reinterpret_cast<const float2*>(A.part_ml + 2 * part(b + lane * du, i)));
-        if (first) {
+        if (b == u0) {  // the row's maximum, over all parts
+          for (int u = lane; u < R.np; u += 32) M = fmaxf(M, __ldcg(A.part_ml + 2 * part(u, i)));
 #pragma unroll
           for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-          first = false;
         }
         const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M), fl = f * ml.y;
 #pragma unroll
@@ -675,13 +710,13 @@ __global__ void __launch_bounds__(128) k_paged_join(const __grid_constant__ Page
       if (lane == 0) s_l[warp] = L;
       __syncthreads();
       if (warp == 0) {
-        L = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
-        for (int w = 1; w < 4; ++w) {
+        for (int w = 1; w < kPjWarps; ++w) {
           const float4 x = s_v[w][lane];
           v.x += x.x;
           v.y += x.y;
           v.z += x.z;
           v.w += x.w;
+          L += s_l[w];
         }
         put(i, M, L, v);
       }
@@ -696,7 +731,7 @@ cudaError_t launch_paged_attention(const PagedAttnParams& A, cudaStream_t s) {
   cfg.gridDim = dim3(want < kPagedMaxCtas ? want : kPagedMaxCtas);
   cfg.blockDim = dim3(kPaThreads);
   const int rows = A.a.max_rows * A.a.group, MT = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  const size_t smem = kPaStages * kPaStageBytes + MT * 4096 + sizeof(PaTable);
+  const size_t smem = kPaStages * kPaStageBytes + (MT == 1 ? 1 : 4) * 4096 + sizeof(PaTable);
   static_assert(2 * (kPaStages * kPaStageBytes + 4 * 4096 + sizeof(PaTable) + 1024) <= 228 * 1024, "two CTAs an SM");
   static_assert(sizeof(PaSeq) * kPagedMaxSeqs <= kPaStages * kPaStageBytes, "the plan fits the ring");
   cfg.dynamicSmemBytes = smem;
@@ -713,7 +748,7 @@ cudaError_t launch_paged_attention(const PagedAttnParams& A, cudaStream_t s) {
   };
   const cudaError_t e = MT == 1 ? run(k_paged_attn<1>) : MT == 2 ? run(k_paged_attn<2>) : run(k_paged_attn<4>);
   if (e != cudaSuccess) return e;
-  cfg.blockDim = dim3(128);
+  cfg.blockDim = dim3(kPjWarps * 32);
   cfg.dynamicSmemBytes = 0;
   max_carveout(k_paged_join);
   return cudaLaunchKernelEx(&cfg, k_paged_join, A, 16 * MT);
