@@ -446,7 +446,7 @@ moe_status moe_workspace_error(void* ws, int* code, void* stream);
  * row_start[b + 1] - 1 (device int32 [n_seqs + 1], not decreasing) are
  * sequence b's, row i of it at position kv_len[b] + i.  A sequence may have
  * no rows.  Rows before row_start[0] or from row_start[n_seqs] on belong to
- * no sequence: nothing of theirs is read or written.
+ * no sequence: nothing of theirs is written.
  *
  * The cache of one layer: position p of sequence b is slot p % page_size of
  * page table[b * max_pages + p / page_size].  kv_len counts the committed

@@ -449,7 +449,9 @@ static moe_status lm_head_impl(const uint16_t* x_norm, int K, int H, const uint1
   a.wait_ns = g_wait_ns.load();
   a.logits = logits;
   cudaError_t e;
-  if (lmhead_stream_fits(K, H)) {
+  if (logits && K > 4) {
+    e = launch_lmhead_logits(a, static_cast<cudaStream_t>(stream));
+  } else if (lmhead_stream_fits(K, H)) {
     e = launch_lmhead_stream(a, static_cast<cudaStream_t>(stream), pdl);
   } else {
     if (norm_eps > 0.f) return MOE_ERR_UNSUPPORTED_SHAPE;  // the row kernel takes normalised rows

@@ -309,6 +309,7 @@ cudaError_t launch_rmsnorm(const uint16_t* x, int K, int H, float eps, uint16_t*
 cudaError_t launch_lmhead(const LmHeadArgs& a, cudaStream_t s, bool pdl);
 bool lmhead_stream_fits(int K, int H);
 cudaError_t launch_lmhead_stream(const LmHeadArgs& a, cudaStream_t s, bool pdl);
+cudaError_t launch_lmhead_logits(const LmHeadArgs& a, cudaStream_t s);  // K > 4, H <= 2048
 cudaError_t launch_router(const RouterArgs& a, cudaStream_t s, bool pdl);
 // One launch of the experts kernel: maps [kMapsPerLayer].
 cudaError_t launch_experts(const ExpertsCommon& c, const CUtensorMap* maps, const LayerDesc& desc, cudaStream_t s,
@@ -391,10 +392,10 @@ struct LogitArgs {
   int tile, ntile;            // tokens per CTA, CTAs per row (set by the launcher)
   int* err;
   unsigned* ticket;           // [R]
-  float* part_v;              // [R][kLogitMaxTiles]
+  float* part_v;              // [R][ntile] each tile's best
   int* part_i;
 };
-constexpr int kLogitTile = 8192;  // most tokens of a CTA
+constexpr int kLogitTile = 16384;  // most tokens of a CTA
 cudaError_t launch_logits(const LogitArgs& a, cudaStream_t s);
 
 // capi.cu: the limit of device waits; the angles and temperature of a moe_attn_pos

@@ -1,0 +1,206 @@
+// lmhead_logits.cu -- the lm_head's logits of 5 to 16 rows, bit for bit those
+// of the argmax kernels: lane l of a warp owns elements 256 j + 8 l + i and
+// accumulates them in element order, the 32 lane sums are added in xor rounds
+// 16, 8, 4, 2, 1.
+//
+// What bounds it: that order leaves the products to the FP32 units (K H V
+// multiply-adds at 128 an SM and clock: 14 us at K 16, H 1024, V 32,003, where
+// the weights' own bytes take 10).  So the other instructions have to be few:
+//  * a warp takes four vocab rows and two rows of x at a time: one
+//    fma.rn.f32x2 (two correctly rounded multiply-adds, so the same bits) per
+//    pair of rows, with the weight in both halves;
+//  * the xor rounds of 32 (row, vocab) sums together: in each round a lane
+//    hands over the half of its sums that its partner keeps, 31 shuffles for
+//    32 sums instead of 160 (a + b = b + a, so again the same bits), and lane
+//    b ends with sum b.
+// Each warp streams its own weights through two 8 KB slots (four rows x up to
+// 1024 columns, one bulk copy a row) and waits for no other warp.
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kLlWarps = 8;
+constexpr int kLlSlots = 2;
+constexpr int kLlRows = 4;      // vocab rows of a warp's step
+constexpr int kLlCols = 1024;   // columns of a slot
+constexpr int kLlSlotBytes = kLlRows * kLlCols * 2;
+constexpr uint64_t kLlDrainNs = 2000000000ull;
+
+struct LlTable {
+  uint64_t full[kLlWarps][kLlSlots];
+  int abort;
+};
+
+__device__ __forceinline__ unsigned long long ll_pair(float lo, float hi) {
+  unsigned long long p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+  return p;
+}
+
+__device__ __forceinline__ void ll_fma2(unsigned long long& d, unsigned long long a, unsigned long long b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
+}
+
+__device__ __forceinline__ float ll_el(const uint4& v, int i) {
+  const uint32_t w = i < 4 ? (i < 2 ? v.x : v.y) : (i < 6 ? v.z : v.w);
+  return (i & 1) ? __uint_as_float(w & 0xFFFF0000u) : __uint_as_float(w << 16);
+}
+
+// The xor-round sums of 32 values: lane b returns the sum of v[b].
+__device__ __forceinline__ float ll_reduce32(float (&v)[32], int lane) {
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) {
+    const bool up = lane & d;
+#pragma unroll
+    for (int k = 0; k < d; ++k) {
+      const float keep = up ? v[k + d] : v[k], give = up ? v[k] : v[k + d];
+      v[k] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, give, d));
+    }
+  }
+  return v[0];
+}
+
+}  // namespace
+
+template <int KR>
+__global__ void __launch_bounds__(kLlWarps * 32, 1) k_lmhead_logits(const __grid_constant__ LmHeadArgs a) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int K = a.K, H = a.H, V = a.V;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  unsigned char* ring = smem + (size_t)warp * kLlSlots * kLlSlotBytes;
+  uint4* xs = reinterpret_cast<uint4*>(smem + (size_t)kLlWarps * kLlSlots * kLlSlotBytes);  // [KR][H] bf16
+  LlTable& T = *reinterpret_cast<LlTable*>(reinterpret_cast<unsigned char*>(xs) + (size_t)KR * H * 2);
+  const int nblk = (H + kLlCols - 1) / kLlCols;
+  const int ngrp = (V + kLlRows - 1) / kLlRows, step = gridDim.x * kLlWarps;
+  const int g0 = warp * gridDim.x + blockIdx.x;  // this warp's groups of rows: g0, g0 + step, ...
+  const int nst = g0 < ngrp ? ((ngrp - 1 - g0) / step + 1) * nblk : 0;
+  volatile int* abort = &T.abort;
+  // stage s: column block s % nblk of the group g0 + (s / nblk) step
+  auto issue = [&](int s, uint64_t pol) {
+    const int grp = g0 + s / nblk * step, c0 = s % nblk * kLlCols;
+    const uint32_t bytes = (uint32_t)min(kLlCols, H - c0) * 2u;
+    const int nr = min(kLlRows, V - grp * kLlRows);
+    uint64_t* bar = &T.full[warp][s % kLlSlots];
+    unsigned char* dst = ring + (size_t)(s % kLlSlots) * kLlSlotBytes;
+    mbar_arrive_expect_tx(bar, bytes * nr);
+    for (int q = 0; q < nr; ++q)
+      bulk_load(dst + q * (kLlCols * 2), a.W + (size_t)(grp * kLlRows + q) * H + c0, bytes, bar, pol);
+  };
+  if (lane == 0) {
+    for (int i = 0; i < kLlSlots; ++i) mbar_init(&T.full[warp][i], 1);
+    if (warp == 0) T.abort = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  uint64_t pol = 0;
+  if (lane == 0) {
+    pol = policy_evict_first();
+    for (int s = 0; s < min(nst, kLlSlots); ++s) issue(s, pol);
+  }
+  pdl_launch_dependents();
+  block_copy_g2s(xs, reinterpret_cast<const uint4*>(a.x), K * H / 8);
+  for (int i = K * H / 8 + threadIdx.x; i < KR * H / 8; i += blockDim.x) xs[i] = make_uint4(0u, 0u, 0u, 0u);
+  __syncthreads();
+
+  unsigned long long acc[kLlRows][KR / 2];  // {row 2p, row 2p + 1} of vocab row q
+  int s = 0;
+  for (; s < nst; ++s) {
+    const int blk = s % nblk;
+    bool ok = !*abort && mbar_wait_bounded(&T.full[warp][s % kLlSlots], (uint32_t)(s / kLlSlots) & 1u, a.wait_ns, abort);
+    if (!__all_sync(0xffffffffu, ok)) {
+      *abort = 1;
+      break;
+    }
+    if (blk == 0) {
+#pragma unroll
+      for (int q = 0; q < kLlRows; ++q)
+#pragma unroll
+        for (int p = 0; p < KR / 2; ++p) acc[q][p] = 0ull;
+    }
+    const uint4* ws = reinterpret_cast<const uint4*>(ring + (size_t)(s % kLlSlots) * kLlSlotBytes);
+    const int nj = min(kLlCols, H - blk * kLlCols) / 256;
+#pragma unroll 1
+    for (int j = 0; j < nj; ++j) {
+      uint4 w[kLlRows];
+#pragma unroll
+      for (int q = 0; q < kLlRows; ++q) w[q] = ws[q * (kLlCols / 8) + j * 32 + lane];
+      const uint4* xj = xs + (blk * (kLlCols / 256) + j) * 32 + lane;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {  // elements 0-3, 4-7 of the lane's eight
+        unsigned long long ww[kLlRows][4];
+#pragma unroll
+        for (int q = 0; q < kLlRows; ++q)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float f = ll_el(w[q], 4 * hf + i);
+            ww[q][i] = ll_pair(f, f);
+          }
+#pragma unroll
+        for (int p = 0; p < KR / 2; ++p) {
+          const uint2 x0 = reinterpret_cast<const uint2*>(xj + (size_t)(2 * p) * (H / 8))[hf];
+          const uint2 x1 = reinterpret_cast<const uint2*>(xj + (size_t)(2 * p + 1) * (H / 8))[hf];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t u0 = i < 2 ? x0.x : x0.y, u1 = i < 2 ? x1.x : x1.y;
+            const unsigned long long xx = (i & 1) ? ll_pair(__uint_as_float(u0 & 0xFFFF0000u), __uint_as_float(u1 & 0xFFFF0000u))
+                                                  : ll_pair(__uint_as_float(u0 << 16), __uint_as_float(u1 << 16));
+#pragma unroll
+            for (int q = 0; q < kLlRows; ++q) ll_fma2(acc[q][p], xx, ww[q][i]);
+          }
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0 && s + kLlSlots < nst) issue(s + kLlSlots, pol);
+    if (blk != nblk - 1) continue;
+    // sums b = q + 4 r of rows r = 8 h .. 8 h + 7, one a lane
+    const int v0 = (g0 + s / nblk * step) * kLlRows;
+#pragma unroll
+    for (int h = 0; h < KR / 8; ++h) {
+      float v[32];
+#pragma unroll
+      for (int b = 0; b < 32; ++b) {
+        const int r = 8 * h + (b >> 2);
+        float lo, hi;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(acc[b & 3][r >> 1]));
+        v[b] = (r & 1) ? hi : lo;
+      }
+      const float l = ll_reduce32(v, lane);
+      const int r = 8 * h + (lane >> 2), q = lane & 3;
+      if (r < K && v0 + q < V) a.logits[(size_t)r * V + v0 + q] = l;
+    }
+  }
+  if (*abort && s < nst) {
+    // this warp's copies still in flight (those of stage s on) land before it leaves
+    if (lane == 0) {
+      for (int i = s; i < min(nst, s + kLlSlots); ++i)
+        mbar_wait_drain(&T.full[warp][i % kLlSlots], (uint32_t)(i / kLlSlots) & 1u, kLlDrainNs);
+      if (a.err) atomicCAS(a.err, 0, (int)MOE_ERR_DEVICE_TIMEOUT);
+    }
+  }
+}
+
+template <int KR>
+static cudaError_t launch_lmhead_logits_t(const LmHeadArgs& a, cudaStream_t s) {
+  const size_t sm = (size_t)kLlWarps * kLlSlots * kLlSlotBytes + (size_t)KR * a.H * 2 + sizeof(LlTable);
+  cudaError_t e = cudaFuncSetAttribute(k_lmhead_logits<KR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+  if (e == cudaSuccess) e = max_carveout(k_lmhead_logits<KR>);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(num_sms());
+  cfg.blockDim = dim3(kLlWarps * 32);
+  cfg.dynamicSmemBytes = sm;
+  cfg.stream = s;
+  // an ordinary launch: the weights are read before the dependency wait
+  return cudaLaunchKernelEx(&cfg, k_lmhead_logits<KR>, a);
+}
+
+// More than 4 rows (fewer are bound by the weights' bytes: k_lmhead_stream).
+cudaError_t launch_lmhead_logits(const LmHeadArgs& a, cudaStream_t s) {
+  return a.K <= 8 ? launch_lmhead_logits_t<8>(a, s) : launch_lmhead_logits_t<16>(a, s);
+}
+
+}  // namespace moe

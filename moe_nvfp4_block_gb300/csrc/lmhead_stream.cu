@@ -66,7 +66,7 @@ template <int KR> struct LsShape {
 
 }  // namespace
 
-// LOGITS: every logit is stored (a.logits) and no argmax taken.
+// LOGITS (K <= 4): every logit is stored (a.logits) and no argmax taken.
 template <int KR, bool LOGITS>
 __global__ void __launch_bounds__(2 * LsShape<KR>::pairs * 32, 1) k_lmhead_stream(const __grid_constant__ LmHeadArgs a) {
   constexpr int kLsPairs = LsShape<KR>::pairs, kLsWarps = 2 * kLsPairs, kLsSlotBytes = LsShape<KR>::slot;
@@ -354,15 +354,10 @@ cudaError_t launch_lmhead_stream(const LmHeadArgs& a0, cudaStream_t s, bool pdl)
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, a);
   };
-  auto pick = [&](auto argmax, auto logits, int pairs, int slot, int rpw) {
-    return a0.logits ? run(logits, pairs, slot, rpw) : run(argmax, pairs, slot, rpw);
-  };
-  if (a0.K <= 4)
-    return pick(k_lmhead_stream<4, false>, k_lmhead_stream<4, true>, LsShape<4>::pairs, LsShape<4>::slot, LsShape<4>::rpw);
-  if (a0.K <= 8)
-    return pick(k_lmhead_stream<8, false>, k_lmhead_stream<8, true>, LsShape<8>::pairs, LsShape<8>::slot, LsShape<8>::rpw);
-  return pick(k_lmhead_stream<16, false>, k_lmhead_stream<16, true>, LsShape<16>::pairs, LsShape<16>::slot,
-              LsShape<16>::rpw);
+  if (a0.logits) return run(k_lmhead_stream<4, true>, LsShape<4>::pairs, LsShape<4>::slot, LsShape<4>::rpw);
+  if (a0.K <= 4) return run(k_lmhead_stream<4, false>, LsShape<4>::pairs, LsShape<4>::slot, LsShape<4>::rpw);
+  if (a0.K <= 8) return run(k_lmhead_stream<8, false>, LsShape<8>::pairs, LsShape<8>::slot, LsShape<8>::rpw);
+  return run(k_lmhead_stream<16, false>, LsShape<16>::pairs, LsShape<16>::slot, LsShape<16>::rpw);
 }
 
 }  // namespace moe

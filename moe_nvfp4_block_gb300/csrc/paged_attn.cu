@@ -146,7 +146,17 @@ __device__ __forceinline__ uint32_t pa_pack(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
-__device__ __forceinline__ float ex2(float x) { return exp2f(x); }
+// 2^x to 2 ulp, 0 below 2^-126.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // mbar_wait_bounded, with several tries before the first look at the clock.
 __device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns, const volatile int* abort) {
@@ -474,7 +484,7 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
             // tanh(z) = 1 - 2 / (e^2z + 1): off by an FP32 rounding of 1, an
             // absolute error, which is what a score needs
             float x = sc[nb][c] * a.scale_log2;
-            if (a.cap_log2 > 0.f) x = a.cap_log2 * (1.f - __fdividef(2.f, ex2(sc[nb][c] * a.cap_in) + 1.f));
+            if (a.cap_log2 > 0.f) x = a.cap_log2 * (1.f - 2.f * rcp(ex2(sc[nb][c] * a.cap_in) + 1.f));
             sc[nb][c] = x + slope[c >> 1] * (float)(pb + 2 * t + (c & 1) - rp[c >> 1]);
           }
         }

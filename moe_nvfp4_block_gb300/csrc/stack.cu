@@ -113,8 +113,7 @@ cudaError_t launch_rmsnorm(const uint16_t* x, int K, int H, float eps, uint16_t*
 // ticket) reduces them in CTA order and writes the tokens.
 constexpr int kLmWarps = 8;
 
-// LOGITS: every logit is stored (a.logits) and no argmax taken.
-template <int KR, bool LOGITS>
+template <int KR>
 __global__ void __launch_bounds__(kLmWarps * 32) k_lmhead_argmax(LmHeadArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float s_bv[kLmWarps][KR];
@@ -176,9 +175,7 @@ __global__ void __launch_bounds__(kLmWarps * 32) k_lmhead_argmax(LmHeadArgs a) {
     for (int r = 0; r < KR; ++r) {
       if (r < K) {
         const float l = warp_sum_xor(acc[r]);
-        if constexpr (LOGITS) {
-          if (lane == r) a.logits[(size_t)r * V + v] = l;
-        } else if (bi[r] == INT_MAX || l > bv[r]) {  // rows arrive in increasing order
+        if (bi[r] == INT_MAX || l > bv[r]) {  // rows arrive in increasing order
           bv[r] = l;
           bi[r] = v;
         }
@@ -187,7 +184,6 @@ __global__ void __launch_bounds__(kLmWarps * 32) k_lmhead_argmax(LmHeadArgs a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) cur[j] = nxt[j];
   }
-  if constexpr (LOGITS) return;
   if (lane == 0) {
 #pragma unroll
     for (int r = 0; r < KR; ++r) {
@@ -252,10 +248,9 @@ cudaError_t launch_lmhead(const LmHeadArgs& a, cudaStream_t s, bool pdl) {
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, a);
   };
-  auto pick = [&](auto argmax, auto logits) { return a.logits ? run(logits) : run(argmax); };
-  if (a.K <= 4) return pick(k_lmhead_argmax<4, false>, k_lmhead_argmax<4, true>);
-  if (a.K <= 8) return pick(k_lmhead_argmax<8, false>, k_lmhead_argmax<8, true>);
-  return pick(k_lmhead_argmax<16, false>, k_lmhead_argmax<16, true>);
+  if (a.K <= 4) return run(k_lmhead_argmax<4>);
+  if (a.K <= 8) return run(k_lmhead_argmax<8>);
+  return run(k_lmhead_argmax<16>);
 }
 
 }  // namespace moe
