@@ -500,7 +500,7 @@ class PagedKV:
         n, nkv, ps, hd = kpages.shape
         dev = kpages.device
         self.kpages, self.vpages, self.table, self.kv_len, self.device = kpages, vpages, table, kv_len, dev
-        self.nkv = nkv
+        self.nkv, self.n_seqs = nkv, kv_len.shape[0]
         self.c = moe_paged_kv(_like(kpages, torch.bfloat16, (n, nkv, ps, hd), "kpages"),
                               _like(vpages, torch.bfloat16, (n, nkv, ps, hd), "vpages", dev),
                               _like(table, torch.int32, (kv_len.shape[0], table.shape[1]), "table", dev),
@@ -520,6 +520,14 @@ class PagedScores:
                                   _like(first, torch.int32, () if first is None else (first.numel(),), "first"),
                                   _like(prefix, torch.int32, () if prefix is None else (prefix.numel(),), "prefix"))
         self._ref = ctypes.byref(self.c)
+        self._none = slopes is None and first is None and prefix is None
+
+    def arrays(self, nq, n_seqs):
+        """(tensor, the length it must have, its name) of those given."""
+        if self._none:
+            return ()
+        return [x for x in ((self.slopes, nq, "slopes"), (self.first, n_seqs, "first"),
+                            (self.prefix, n_seqs, "prefix")) if x[0] is not None]
 
 
 def paged_workspace(kv: PagedKV, max_rows: int, nq: int) -> torch.Tensor:
@@ -541,16 +549,24 @@ def _strided(t, what, kv, n_rows, width=None):
 
 
 def _starts(kv, row_start):
-    n = kv.c.n_seqs + 1
+    n = kv.n_seqs + 1
     if row_start.dtype != torch.int32 or row_start.shape != (n,) or row_start.device != kv.device or \
             not row_start.is_contiguous():
         raise ValueError(f"row_start must be an int32 tensor [{n}] on {kv.device}")
     return row_start.data_ptr()
 
 
-def _stream_on(device, stream):
-    """The given stream, or the current one of the tensors' device."""
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+def _call(what, device, stream, f, *args):
+    """f(*args, stream) on the tensors' device, on its current stream if none is given."""
+    i = device.index
+    s = torch._C._cuda_getCurrentRawStream(i) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == i:
+        status = f(*args, s)
+    else:
+        with torch.cuda.device(device):
+            status = f(*args, s)
+    if status:
+        raise MoeError(status, what)
 
 
 def _heads(t, what):
@@ -574,10 +590,8 @@ def moe_paged_kv_append(kv: PagedKV, k_new, v_new, row_start, ws, q=None, q_out=
         nq = _heads(q, "q")
         qp, qs = _strided(q, "q", kv, T, nq * 128)
         op, os_ = _strided(q_out, "q_out", kv, T, nq * 128)
-    with torch.cuda.device(kv.device):
-        _check(lib.moe_paged_kv_append(kv._ref, qp, qs, kp, ks, vp, vs, T, nq, _starts(kv, row_start),
-                                       None if pos is None else ctypes.byref(pos), op, os_, ws.data_ptr(), ws.numel(),
-                                       _stream_on(kv.device, stream)), "moe_paged_kv_append")
+    _call("moe_paged_kv_append", kv.device, stream, lib.moe_paged_kv_append, kv._ref, qp, qs, kp, ks, vp, vs, T, nq,
+          _starts(kv, row_start), None if pos is None else ctypes.byref(pos), op, os_, ws.data_ptr(), ws.numel())
 
 
 def moe_paged_attention(kv: PagedKV, q, row_start, o, ws, max_rows, scores: PagedScores | None = None, lse=None,
@@ -589,16 +603,13 @@ def moe_paged_attention(kv: PagedKV, q, row_start, o, ws, max_rows, scores: Page
     op, os_ = _strided(o, "o", kv, T, nq * 128)
     ref = None
     if scores is not None:
-        for t, n, what in ((scores.slopes, nq, "slopes"), (scores.first, kv.c.n_seqs, "first"),
-                           (scores.prefix, kv.c.n_seqs, "prefix")):
-            if t is not None and (t.numel() != n or t.device != kv.device):
+        for t, n, what in scores.arrays(nq, kv.n_seqs):
+            if t.numel() != n or t.device != kv.device:
                 raise ValueError(f"{what} must have {n} values on {kv.device}")
         ref = scores._ref
     lp = _like(lse, torch.float32, (T, nq), "lse", kv.device)
-    with torch.cuda.device(kv.device):
-        _check(lib.moe_paged_attention(kv._ref, qp, qs, T, max_rows, nq, _starts(kv, row_start), ref, op, os_, lp,
-                                       ws.data_ptr(), ws.numel(), _stream_on(kv.device, stream)),
-               "moe_paged_attention")
+    _call("moe_paged_attention", kv.device, stream, lib.moe_paged_attention, kv._ref, qp, qs, T, max_rows, nq,
+          _starts(kv, row_start), ref, op, os_, lp, ws.data_ptr(), ws.numel())
 
 
 class LogitRules:
@@ -657,12 +668,11 @@ def moe_logits_constrain(logits, rules: LogitRules | None, ws, out=None, tok=Non
                 (a is not None and a.shape[-1] != (V + 31) // 32)):
             raise ValueError(f"the rules are not for {R} rows of {V} logits on {dev}")
         ref = rules._ref
-    with torch.cuda.device(dev):
-        _check(lib.moe_logits_constrain(
-            logits.data_ptr(), MOE_LOGITS_BF16 if logits.dtype == torch.bfloat16 else MOE_LOGITS_F32, logits.stride(0),
-            R, V, ref, None if out is None else out.data_ptr(), 0 if out is None else out.stride(0),
-            _like(tok, torch.int32, (R,), "tok", dev), _like(best, torch.float32, (R,), "best", dev), ws.data_ptr(),
-            ws.numel(), _stream_on(dev, stream)), "moe_logits_constrain")
+    _call("moe_logits_constrain", dev, stream, lib.moe_logits_constrain, logits.data_ptr(),
+          MOE_LOGITS_BF16 if logits.dtype == torch.bfloat16 else MOE_LOGITS_F32, logits.stride(0), R, V, ref,
+          None if out is None else out.data_ptr(), 0 if out is None else out.stride(0),
+          _like(tok, torch.int32, (R,), "tok", dev), _like(best, torch.float32, (R,), "best", dev), ws.data_ptr(),
+          ws.numel())
 
 
 def moe_workspace_error(ws, stream=None) -> int:

@@ -130,13 +130,14 @@ bool moe::encode_kv_map(CUtensorMap* m, const uint16_t* cache, int nkv, int C, b
 }
 
 // Map over pages of a KV cache seen as `rows` rows of 128 dims: one box is
-// box_rows rows, laid out as [dim half][row][64 dims] with the 128-byte swizzle.
-bool moe::encode_page_map(CUtensorMap* m, const uint16_t* pages, int64_t rows, int box_rows) {
+// box_rows rows of one or both dim halves, laid out as [dim half][row][64
+// dims] with the 128-byte swizzle.
+bool moe::encode_page_map(CUtensorMap* m, const uint16_t* pages, int64_t rows, int box_rows, int box_halves) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {64, (cuuint64_t)rows, 2};
   cuuint64_t strides[2] = {256, 128};
-  cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_halves};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(pages), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

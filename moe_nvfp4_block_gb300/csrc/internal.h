@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/moe_verify.h"
 
 namespace moe {
@@ -378,7 +380,11 @@ struct PagedAttnParams {
   float* part_ml;   // [kPagedMaxCtas][2][padded rows][2]
   uint64_t wait_ns;
 };
-bool encode_page_map(CUtensorMap* m, const uint16_t* pages, int64_t rows, int box_rows);
+bool encode_page_map(CUtensorMap* m, const uint16_t* pages, int64_t rows, int box_rows, int box_halves);
+// The form for `rows` query rows a KV head: tcgen05 (its maps' boxes are one
+// dim half) for more than 32, mma.sync (both halves) up to 32.
+inline bool paged_attention_tc(int rows) { return rows > 32; }
+cudaError_t launch_paged_attention_tc(const PagedAttnParams& a, int padded_rows, cudaStream_t s);
 cudaError_t launch_paged_attention(const PagedAttnParams& a, cudaStream_t s);
 
 struct LogitArgs {
@@ -395,7 +401,7 @@ struct LogitArgs {
   float* part_v;              // [R][ntile] each tile's best
   int* part_i;
 };
-constexpr int kLogitTile = 16384;  // most tokens of a CTA
+constexpr int kLogitTile = 65536;  // most tokens of a CTA
 cudaError_t launch_logits(const LogitArgs& a, cudaStream_t s);
 
 // capi.cu: the limit of device waits; the angles and temperature of a moe_attn_pos
@@ -412,6 +418,22 @@ template <typename Kern>
 inline cudaError_t max_carveout(Kern kern) {
   return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
                               (int)cudaSharedmemCarveoutMaxShared);
+}
+
+// The shared-memory limit and the carveout of a kernel, set on a device's
+// first launch of it (each attribute costs a driver call of 0.2-0.4 us).
+template <auto KERN>
+inline cudaError_t prepare_kernel(int smem) {
+  static std::atomic<uint64_t> done{0};  // a bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  if (smem > 0) e = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = max_carveout(KERN);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 }  // namespace moe

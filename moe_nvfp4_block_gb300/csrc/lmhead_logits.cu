@@ -13,8 +13,8 @@
 //    hands over the half of its sums that its partner keeps, 31 shuffles for
 //    32 sums instead of 160 (a + b = b + a, so again the same bits), and lane
 //    b ends with sum b.
-// Each warp streams its own weights through two 8 KB slots (four rows x up to
-// 1024 columns, one bulk copy a row) and waits for no other warp.
+// Each warp streams its own weights through two 4 KB slots (four rows x up to
+// 512 columns, one bulk copy a row) and waits for no other warp.
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -22,10 +22,10 @@ namespace moe {
 
 namespace {
 
-constexpr int kLlWarps = 8;
+constexpr int kLlWarps = 12;
 constexpr int kLlSlots = 2;
 constexpr int kLlRows = 4;      // vocab rows of a warp's step
-constexpr int kLlCols = 1024;   // columns of a slot
+constexpr int kLlCols = 512;    // columns of a slot
 constexpr int kLlSlotBytes = kLlRows * kLlCols * 2;
 constexpr uint64_t kLlDrainNs = 2000000000ull;
 
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kLlWarps * 32, 1) k_lmhead_logits(const __grid
   const int K = a.K, H = a.H, V = a.V;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   unsigned char* ring = smem + (size_t)warp * kLlSlots * kLlSlotBytes;
-  uint4* xs = reinterpret_cast<uint4*>(smem + (size_t)kLlWarps * kLlSlots * kLlSlotBytes);  // [KR][H] bf16
+  uint2* xs = reinterpret_cast<uint2*>(smem + (size_t)kLlWarps * kLlSlots * kLlSlotBytes);  // [KR][H] bf16
   LlTable& T = *reinterpret_cast<LlTable*>(reinterpret_cast<unsigned char*>(xs) + (size_t)KR * H * 2);
   const int nblk = (H + kLlCols - 1) / kLlCols;
   const int ngrp = (V + kLlRows - 1) / kLlRows, step = gridDim.x * kLlWarps;
@@ -101,8 +101,14 @@ __global__ void __launch_bounds__(kLlWarps * 32, 1) k_lmhead_logits(const __grid
     for (int s = 0; s < min(nst, kLlSlots); ++s) issue(s, pol);
   }
   pdl_launch_dependents();
-  block_copy_g2s(xs, reinterpret_cast<const uint4*>(a.x), K * H / 8);
-  for (int i = K * H / 8 + threadIdx.x; i < KR * H / 8; i += blockDim.x) xs[i] = make_uint4(0u, 0u, 0u, 0u);
+  // x in planes [row][256 columns][first or second half of a lane's eight][lane][4]:
+  // a warp's 8-byte reads are consecutive (all banks)
+  for (int i = threadIdx.x; i < KR * H / 8; i += blockDim.x) {
+    const uint4 v = i < K * H / 8 ? __ldcg(reinterpret_cast<const uint4*>(a.x) + i) : make_uint4(0u, 0u, 0u, 0u);
+    uint2* at = xs + (size_t)(i >> 5) * 64 + (i & 31);
+    at[0] = make_uint2(v.x, v.y);
+    at[32] = make_uint2(v.z, v.w);
+  }
   __syncthreads();
 
   unsigned long long acc[kLlRows][KR / 2];  // {row 2p, row 2p + 1} of vocab row q
@@ -127,7 +133,7 @@ __global__ void __launch_bounds__(kLlWarps * 32, 1) k_lmhead_logits(const __grid
       uint4 w[kLlRows];
 #pragma unroll
       for (int q = 0; q < kLlRows; ++q) w[q] = ws[q * (kLlCols / 8) + j * 32 + lane];
-      const uint4* xj = xs + (blk * (kLlCols / 256) + j) * 32 + lane;
+      const uint2* xj = xs + (blk * (kLlCols / 256) + j) * 64 + lane;
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {  // elements 0-3, 4-7 of the lane's eight
         unsigned long long ww[kLlRows][4];
@@ -140,8 +146,7 @@ __global__ void __launch_bounds__(kLlWarps * 32, 1) k_lmhead_logits(const __grid
           }
 #pragma unroll
         for (int p = 0; p < KR / 2; ++p) {
-          const uint2 x0 = reinterpret_cast<const uint2*>(xj + (size_t)(2 * p) * (H / 8))[hf];
-          const uint2 x1 = reinterpret_cast<const uint2*>(xj + (size_t)(2 * p + 1) * (H / 8))[hf];
+          const uint2 x0 = xj[2 * p * (H / 4) + 32 * hf], x1 = xj[(2 * p + 1) * (H / 4) + 32 * hf];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint32_t u0 = i < 2 ? x0.x : x0.y, u1 = i < 2 ? x1.x : x1.y;
@@ -186,8 +191,8 @@ __global__ void __launch_bounds__(kLlWarps * 32, 1) k_lmhead_logits(const __grid
 template <int KR>
 static cudaError_t launch_lmhead_logits_t(const LmHeadArgs& a, cudaStream_t s) {
   const size_t sm = (size_t)kLlWarps * kLlSlots * kLlSlotBytes + (size_t)KR * a.H * 2 + sizeof(LlTable);
-  cudaError_t e = cudaFuncSetAttribute(k_lmhead_logits<KR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
-  if (e == cudaSuccess) e = max_carveout(k_lmhead_logits<KR>);
+  constexpr int most = kLlWarps * kLlSlots * kLlSlotBytes + KR * 2048 * 2 + (int)sizeof(LlTable);
+  const cudaError_t e = prepare_kernel<k_lmhead_logits<KR>>(most);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(num_sms());

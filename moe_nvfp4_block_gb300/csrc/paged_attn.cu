@@ -36,8 +36,7 @@
 // an infinite or NaN v, a slice with hidden positions is looked over for such
 // values first and, with any, summed element by element over the visible
 // positions alone.
-#include "internal.h"
-#include "ptx.cuh"
+#include "paged_attn.cuh"
 
 namespace moe {
 
@@ -45,85 +44,12 @@ namespace {
 
 constexpr int kPaWarps = 8;                      // compute warps
 constexpr int kPaThreads = (kPaWarps + 1) * 32;  // and the producer
-constexpr int kPaChunk = 64;
 constexpr int kPaStages = 3;
-constexpr int kPaHalf = kPaChunk * 256;          // a stage's keys (or values)
-constexpr int kPaStageBytes = 2 * kPaHalf;
-constexpr int kPaUnit = 1;                       // slots before a unit's chunks
-constexpr uint64_t kPaDrainNs = 2000000000ull;
-
-// A chunk as its stage's readers see it.
-struct PaDesc {
-  int q0, n, len, kvh;       // the sequence's first row, rows, committed length; KV head
-  int pos0, first, prefix;   // the chunk's first position; the sequence's limits
-  int flags;                 // kPaLast: the segment's last chunk; kPaEnd; kPaAny, kPaAll
-  int cf, np;                // np > 1: a cut unit, whose first CTA is cf and whose parts are np
-  int slot, pad;             // where this CTA's part goes (0 / 1)
-};
-constexpr int kPaLast = 1, kPaEnd = 2;  // kPaEnd: no chunk, the CTA is done
-constexpr int kPaAny = 4, kPaAll = 8;   // bit of the first of four 16-position slices: some row sees
-                                        // some of it / every row sees all of it
 
 struct PaTable {
-  uint64_t full[kPaStages];
-  uint64_t empty[kPaStages];
-  uint64_t told[kPaStages];  // the description is written (the data may still be on its way)
-  PaDesc desc[kPaStages];
-  int abort;
+  PaRing<kPaStages> ring;
   float m[kPaWarps * 16];  // [tile][row][part]: maxima of the parts' scores; at a segment's end their sums
 };
-
-// A sequence of the call: its rows, and the chunks that hold their visible
-// positions: np of the kept prefix from cp, then those from cm on.
-struct PaSeq {
-  int q0, n, len, first, prefix;
-  int cp, np, cm, nch;
-};
-
-__device__ __forceinline__ PaSeq pa_seq(const PagedAttnArgs& a, int b, int* err) {
-  const PagedRows& P = a.p;
-  PaSeq s{};
-  s.q0 = P.start[b];
-  const int q1 = P.start[b + 1];
-  s.len = P.kv_len[b];
-  s.first = a.first ? max(0, a.first[b]) : 0;
-  s.prefix = a.prefix && a.window > 0 ? a.prefix[b] : 0;
-  if (q1 == s.q0) return s;
-  int e = 0;
-  if (s.q0 < 0 || q1 < s.q0 || q1 > P.T || q1 - s.q0 > a.max_rows || s.len < 0) e = MOE_ERR_INVALID_ARG;
-  else if ((long long)s.len + (q1 - s.q0) > (long long)P.max_pages << P.lps) e = MOE_ERR_CAPACITY;
-  if (e) {
-    if (err) atomicCAS(err, 0, e);
-    return s;
-  }
-  s.n = q1 - s.q0;
-  const int hi = s.len + s.n;
-  s.first = min(s.first, hi);
-  s.prefix = min(s.prefix, hi);
-  const int lo = a.window > 0 ? max(s.first, s.len - a.window + 1) : s.first;
-  s.cm = lo / kPaChunk;
-  s.nch = lo < hi ? (hi - 1) / kPaChunk + 1 - s.cm : 0;
-  if (s.prefix > s.first && lo > s.first) {
-    s.cp = s.first / kPaChunk;
-    const int end = min((min(s.prefix, lo) - 1) / kPaChunk + 1, s.cm);
-    s.np = max(0, end - s.cp);
-    s.nch += s.np;
-  }
-  if (s.nch == 0) {  // rows that see nothing still have an output
-    s.cm = 0;
-    s.nch = 1;
-  }
-  return s;
-}
-
-// Whether some row sees a position of [p0, p1]; whether every row sees all.
-__device__ __forceinline__ bool pa_any(int len, int n, int first, int prefix, int window, int p0, int p1) {
-  const int hi = len + n, lo = window > 0 ? max(first, len - window + 1) : first;
-  return (p0 < hi && p1 >= lo) || (max(p0, first) < prefix && p1 >= first);
-}
-__device__ __forceinline__ bool pa_all(int len, int n, int first, int prefix, int window, int p0, int p1) {
-  return p0 >= first && p1 <= len && (window == 0 || p0 > len + n - 1 - window || p1 < prefix);
-}
 
 __device__ __forceinline__ void pa_ldsm(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -141,32 +67,6 @@ __device__ __forceinline__ void pa_mma(float (&d)[4], const uint32_t (&a)[4], ui
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pa_pack(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-// 2^x to 2 ulp, 0 below 2^-126.
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// mbar_wait_bounded, with several tries before the first look at the clock.
-__device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns, const volatile int* abort) {
-  if (limit_ns == 0) return false;
-#pragma unroll 1
-  for (int i = 0; i < 16; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait_bounded(bar, parity, limit_ns, abort);
-}
-
 // Barrier of a tile's warps that also tells whether one has given up.  A warp
 // that gives up (a wait ran out) takes part once more, with `fail`, and
 // leaves; so does every warp at the end: each instance has all of them.
@@ -198,11 +98,11 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
   const int lbr = min(P.lps, 6), br = 1 << lbr;  // positions of a box
 
   if (threadIdx.x == 0) {
-    T.abort = 0;
+    T.ring.abort = 0;
     for (int i = 0; i < kPaStages; ++i) {
-      mbar_init(&T.full[i], 1);
-      mbar_init(&T.empty[i], kPaWarps);
-      mbar_init(&T.told[i], 1);
+      mbar_init(&T.ring.full[i], 1);
+      mbar_init(&T.ring.empty[i], kPaWarps);
+      mbar_init(&T.ring.told[i], 1);
     }
     fence_mbar_init();
     prefetch_tensormap(&A.km);
@@ -214,145 +114,17 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
   for (int b = threadIdx.x; b < P.n_seqs; b += kPaThreads) plan[b] = pa_seq(a, b, cta == 0 ? P.err : nullptr);
   __syncthreads();
 
-  volatile int* abort = &T.abort;
+  volatile int* abort = &T.ring.abort;
   if (warp == kPaWarps) {
-    // ---------------------------------------------------------------- producer
-    // lane l sums the sequences [l k, (l + 1) k); the lane that holds the
-    // CTA's first slot finds its sequence
-    auto slots = [&](int nch) { return nch > 0 ? (long long)P.nkv * (nch + kPaUnit) : 0LL; };
-    const int k = (P.n_seqs + 31) / 32;
-    long long sum = 0;
-    for (int i = 0; i < k; ++i)
-      if (lane * k + i < P.n_seqs) sum += slots(plan[lane * k + i].nch);
-    long long inc = sum;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long o = __shfl_up_sync(0xffffffffu, inc, d);
-      if (lane >= d) inc += o;
-    }
-    const long long W = __shfl_sync(0xffffffffu, inc, 31);
-    // no more CTAs than slots: every CTA inside a cut unit has a part of it
-    const int G = (int)min((long long)gridDim.x, W);
-    const bool small = W < 1 << 22;  // 32-bit divisions do
-    auto div = [&](long long x, long long y) {
-      return small ? (long long)((unsigned)x / (unsigned)y) : x / y;
-    };
-    const long long w0 = cta < G ? div(cta * W, G) : W, w1 = cta < G ? div((cta + 1) * W, G) : W;
-    long long base = inc - sum;
-    int b = lane * k;
-    const bool mine = base <= w0 && w0 < inc;
-    if (mine)
-      while (base + slots(plan[b].nch) <= w0) base += slots(plan[b++].nch);
-    const unsigned who = __ballot_sync(0xffffffffu, mine);
-    const int src = who ? __ffs(who) - 1 : 0;
-    b = __shfl_sync(0xffffffffu, b, src);
-    base = __shfl_sync(0xffffffffu, base, src);
-    PaSeq s{};
-    if (w0 < w1) s = plan[b];
-    // the plan's memory becomes the ring's: its reads before the async writes
-    __syncwarp();
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-
+    unsigned char* ring = smem;
     const uint64_t pol = policy_evict_first();
-    const int lnb = 6 - lbr;  // log2 of a chunk's boxes
-    int st = 0;
-    // A stage: its description (written by lane 0) and its bytes; false: given up.
-    auto begin = [&]() {
-      const int sl = st % kPaStages;
-      bool ok = true;
-      if (st >= kPaStages)
-        ok = !*abort && pa_wait(&T.empty[sl], (uint32_t)(st / kPaStages - 1) & 1u, A.wait_ns, abort);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) *abort = 1;
-      return ok;
-    };
-    bool live = true;
-    int kvh = s.nch > 0 ? (int)div(w0 - base, s.nch + kPaUnit) : 0;
-    // page cache: lane l holds box l & (boxes - 1) of chunk cj + (l >> lnb) of sequence cb
-    int cb = -1, cj = 0, crow = 0;
-    bool cload = false;
-    while (live) {
-      const int span = s.nch + kPaUnit;
-      const long long rs = base + (long long)kvh * span + kPaUnit, re = rs + s.nch;  // the unit's chunks
-      if (rs >= w1 || w0 >= w1) break;
-      const int j0 = rs >= w0 ? 0 : (int)(w0 - rs), j1 = (int)(min(re, w1) - rs);
-      int cf = 0, np = 1;
-      if (rs < w0 || re > w1) {
-        cf = (int)div((rs + 1) * G - 1, W);
-        np = (int)div(re * G - 1, W) - cf + 1;
-      }
-      for (int j = j0; j < j1; ++j) {
-        if (b != cb || j < cj || j >= cj + (32 >> lnb)) {
-          cb = b;
-          cj = j;
-          const int c = j + (lane >> lnb);
-          const int p0 = (c < s.np ? s.cp + c : s.cm + c - s.np) * kPaChunk + ((lane & ((1 << lnb) - 1)) << lbr);
-          cload = c < s.nch && pa_any(s.len, s.n, s.first, s.prefix, a.window, p0, p0 + br - 1);
-          if (cload) {
-            int page = P.table[(size_t)b * P.max_pages + (p0 >> P.lps)];
-            if (page < 0 || page >= P.n_pages) {
-              atomicCAS(P.err, 0, (int)MOE_ERR_INVALID_ARG);
-              page = 0;
-            }
-            crow = (page * P.nkv << P.lps) + (p0 & ((1 << P.lps) - 1));
-          }
-        }
-        live = begin();
-        if (!live) break;
-        const bool load = cload && (lane >> lnb) == j - cj;
-        const unsigned boxes = __ballot_sync(0xffffffffu, load);
-        const int pos0 = (j < s.np ? s.cp + j : s.cm + j - s.np) * kPaChunk, sp = pos0 + 16 * (lane & 3);
-        const unsigned any = __ballot_sync(0xffffffffu, pa_any(s.len, s.n, s.first, s.prefix, a.window, sp, sp + 15));
-        const unsigned all = __ballot_sync(0xffffffffu, pa_all(s.len, s.n, s.first, s.prefix, a.window, sp, sp + 15));
-        const int sl = st % kPaStages;
-        if (lane == 0) {
-          PaDesc& d = T.desc[sl];
-          d.q0 = s.q0;
-          d.n = s.n;
-          d.len = s.len;
-          d.kvh = kvh;
-          d.pos0 = pos0;
-          d.first = s.first;
-          d.prefix = s.prefix;
-          d.flags = (j == j1 - 1 ? kPaLast : 0) | (int)(any & 15u) << kPaAny | (int)(all & 15u) << kPaAll;
-          d.cf = cf;
-          d.np = np;
-          d.slot = rs >= w0;
-          mbar_arrive(&T.told[sl]);
-          mbar_arrive_expect_tx(&T.full[sl], __popc(boxes) * (uint32_t)(br * 512));
-        }
-        __syncwarp();
-        if (load) {
-          unsigned char* dst = smem + (size_t)sl * kPaStageBytes + (lane & ((1 << lnb) - 1)) * (br * 256);
-          const int row = crow + (kvh << P.lps);
-          tma_load_3d(dst, &A.km, 0, row, 0, &T.full[sl], pol);
-          tma_load_3d(dst + kPaHalf, &A.vm, 0, row, 0, &T.full[sl], pol);
-        }
-        ++st;
-      }
-      if (!live || re >= w1) break;
-      if (++kvh == P.nkv) {
-        base += (long long)P.nkv * span;
-        kvh = 0;
-        do s = pa_seq(a, ++b, nullptr);
-        while (s.nch == 0);
-      }
-    }
-    if (live && (live = begin())) {
-      if (lane == 0) {
-        T.desc[st % kPaStages].flags = kPaEnd;
-        mbar_arrive(&T.told[st % kPaStages]);
-        mbar_arrive(&T.full[st % kPaStages]);
-      }
-      ++st;
-    }
-    __syncwarp();
+    const int st = pa_produce(A, T.ring, plan, cta, lane, [&](int sl, int box, int row, uint64_t* bar) {
+      unsigned char* dst = ring + (size_t)sl * kPaStageBytes + box * (br * 256);
+      tma_load_3d(dst, &A.km, 0, row, 0, bar, pol);
+      tma_load_3d(dst + kPaHalf, &A.vm, 0, row, 0, bar, pol);
+    });
     __syncthreads();  // every warp is done with the ring
-    if (*abort && lane == 0) {
-      atomicCAS(P.err, 0, (int)MOE_ERR_DEVICE_TIMEOUT);
-      for (int i = max(0, st - kPaStages); i < st; ++i)
-        mbar_wait_drain(&T.full[i % kPaStages], (uint32_t)(i / kPaStages) & 1u, kPaDrainNs);
-    }
+    if (*abort && lane == 0) pa_drain(T.ring, st, P.err);
     return;
   }
 
@@ -373,10 +145,10 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
   for (int st = 0;; ++st) {
     const int sl = st % kPaStages;
     const uint32_t par = (uint32_t)(st / kPaStages) & 1u;
-    const PaDesc& D = T.desc[sl];
+    const PaDesc& D = T.ring.desc[sl];
     bool ok = !*abort;
     if (fresh) {  // the rows are loaded while the keys are on their way
-      ok = ok && pa_wait(&T.told[sl], par, A.wait_ns, abort);
+      ok = ok && pa_wait(&T.ring.told[sl], par, A.wait_ns, abort);
       ok = __all_sync(0xffffffffu, ok);
       if (ok && !(D.flags & kPaEnd)) {
 #pragma unroll
@@ -420,7 +192,7 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
         }
       }
     }
-    ok = ok && pa_wait(&T.full[sl], par, A.wait_ns, abort);
+    ok = ok && pa_wait(&T.ring.full[sl], par, A.wait_ns, abort);
     if (!__all_sync(0xffffffffu, ok)) {
       *abort = 1;
       sync(true);
@@ -604,7 +376,7 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
     }
     if (!(flags & kPaLast)) {
       __syncwarp();
-      if (lane == 0) mbar_arrive(&T.empty[sl]);
+      if (lane == 0) mbar_arrive(&T.ring.empty[sl]);
       continue;
     }
 
@@ -647,7 +419,7 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
     }
     if (D.np > 1 && threadIdx.x == 0) A.rec[cta * 2 + D.slot] = {D.cf, D.np, D.q0, D.n, D.kvh};
     __syncwarp();
-    if (lane == 0) mbar_arrive(&T.empty[sl]);
+    if (lane == 0) mbar_arrive(&T.ring.empty[sl]);
   }
   __syncthreads();  // the ring is free
 }
@@ -737,7 +509,7 @@ __global__ void __launch_bounds__(kPjWarps * 32) k_paged_join(const __grid_const
 
 cudaError_t launch_paged_attention(const PagedAttnParams& A, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  const int want = 2 * num_sms();
+  const int want = paged_attention_tc(A.a.max_rows * A.a.group) ? num_sms() : 2 * num_sms();
   cfg.gridDim = dim3(want < kPagedMaxCtas ? want : kPagedMaxCtas);
   cfg.blockDim = dim3(kPaThreads);
   const int rows = A.a.max_rows * A.a.group, MT = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
@@ -751,17 +523,16 @@ cudaError_t launch_paged_attention(const PagedAttnParams& A, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto run = [&](auto kern) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess) e = max_carveout(kern);
-    return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, kern, A) : e;
-  };
-  const cudaError_t e = MT == 1 ? run(k_paged_attn<1>) : MT == 2 ? run(k_paged_attn<2>) : run(k_paged_attn<4>);
+  auto run = [&](auto kern, cudaError_t e) { return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, kern, A) : e; };
+  const cudaError_t e = paged_attention_tc(rows) ? launch_paged_attention_tc(A, 16 * MT, s)
+                        : MT == 1 ? run(k_paged_attn<1>, prepare_kernel<k_paged_attn<1>>((int)smem))
+                        : MT == 2 ? run(k_paged_attn<2>, prepare_kernel<k_paged_attn<2>>((int)smem))
+                                  : run(k_paged_attn<4>, prepare_kernel<k_paged_attn<4>>((int)smem));
   if (e != cudaSuccess) return e;
   cfg.blockDim = dim3(kPjWarps * 32);
   cfg.dynamicSmemBytes = 0;
-  max_carveout(k_paged_join);
-  return cudaLaunchKernelEx(&cfg, k_paged_join, A, 16 * MT);
+  const cudaError_t ej = prepare_kernel<k_paged_join>(0);
+  return ej == cudaSuccess ? cudaLaunchKernelEx(&cfg, k_paged_join, A, 16 * MT) : ej;
 }
 
 }  // namespace moe

@@ -1,0 +1,267 @@
+// paged_attn.cuh -- what the two forms of the paged attention share: how a
+// call's work is listed and cut, and the producer warp that walks it.
+#pragma once
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kPaChunk = 64;                     // positions of a chunk
+constexpr int kPaHalf = kPaChunk * 256;          // a stage's keys (or values)
+constexpr int kPaStageBytes = 2 * kPaHalf;
+constexpr int kPaUnit = 1;                       // slots before a unit's chunks
+constexpr uint64_t kPaDrainNs = 2000000000ull;
+
+// A chunk as its stage's readers see it.
+struct PaDesc {
+  int q0, n, len, kvh;       // the sequence's first row, rows, committed length; KV head
+  int pos0, first, prefix;   // the chunk's first position; the sequence's limits
+  int flags;                 // kPaLast: the segment's last chunk; kPaEnd; kPaAny, kPaAll
+  int cf, np;                // np > 1: a cut unit, whose first CTA is cf and whose parts are np
+  int slot, pad;             // where this CTA's part goes (0 / 1)
+};
+constexpr int kPaLast = 1, kPaEnd = 2;  // kPaEnd: no chunk, the CTA is done
+constexpr int kPaAny = 4, kPaAll = 8;   // bit of the first of four 16-position slices: some row sees
+                                        // some of it / every row sees all of it
+
+template <int STAGES>
+struct PaRing {
+  uint64_t full[STAGES];
+  uint64_t empty[STAGES];
+  uint64_t told[STAGES];  // the description is written (the data may still be on its way)
+  PaDesc desc[STAGES];
+  int abort;
+};
+
+// A sequence of the call: its rows, and the chunks that hold their visible
+// positions: np of the kept prefix from cp, then those from cm on.
+struct PaSeq {
+  int q0, n, len, first, prefix;
+  int cp, np, cm, nch;
+};
+
+__device__ __forceinline__ PaSeq pa_seq(const PagedAttnArgs& a, int b, int* err) {
+  const PagedRows& P = a.p;
+  PaSeq s{};
+  s.q0 = P.start[b];
+  const int q1 = P.start[b + 1];
+  s.len = P.kv_len[b];
+  s.first = a.first ? max(0, a.first[b]) : 0;
+  s.prefix = a.prefix && a.window > 0 ? a.prefix[b] : 0;
+  if (q1 == s.q0) return s;
+  int e = 0;
+  if (s.q0 < 0 || q1 < s.q0 || q1 > P.T || q1 - s.q0 > a.max_rows || s.len < 0) e = MOE_ERR_INVALID_ARG;
+  else if ((long long)s.len + (q1 - s.q0) > (long long)P.max_pages << P.lps) e = MOE_ERR_CAPACITY;
+  if (e) {
+    if (err) atomicCAS(err, 0, e);
+    return s;
+  }
+  s.n = q1 - s.q0;
+  const int hi = s.len + s.n;
+  s.first = min(s.first, hi);
+  s.prefix = min(s.prefix, hi);
+  const int lo = a.window > 0 ? max(s.first, s.len - a.window + 1) : s.first;
+  s.cm = lo / kPaChunk;
+  s.nch = lo < hi ? (hi - 1) / kPaChunk + 1 - s.cm : 0;
+  if (s.prefix > s.first && lo > s.first) {
+    s.cp = s.first / kPaChunk;
+    const int end = min((min(s.prefix, lo) - 1) / kPaChunk + 1, s.cm);
+    s.np = max(0, end - s.cp);
+    s.nch += s.np;
+  }
+  if (s.nch == 0) {  // rows that see nothing still have an output
+    s.cm = 0;
+    s.nch = 1;
+  }
+  return s;
+}
+
+// Whether some row sees a position of [p0, p1]; whether every row sees all.
+__device__ __forceinline__ bool pa_any(int len, int n, int first, int prefix, int window, int p0, int p1) {
+  const int hi = len + n, lo = window > 0 ? max(first, len - window + 1) : first;
+  return (p0 < hi && p1 >= lo) || (max(p0, first) < prefix && p1 >= first);
+}
+__device__ __forceinline__ bool pa_all(int len, int n, int first, int prefix, int window, int p0, int p1) {
+  return p0 >= first && p1 <= len && (window == 0 || p0 > len + n - 1 - window || p1 < prefix);
+}
+
+__device__ __forceinline__ uint32_t pa_pack(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// 2^x to 2 ulp, 0 below 2^-126.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// mbar_wait_bounded, with several tries before the first look at the clock.
+__device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns, const volatile int* abort) {
+  if (limit_ns == 0) return false;
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait_bounded(bar, parity, limit_ns, abort);
+}
+
+// The producer warp: the CTA's share of the call's slots (plan: every
+// sequence), chunk by chunk into the ring; put(stage, box, row, barrier)
+// loads the box of br cache rows from `row` on (keys and values).  Ends with
+// a stage that says kPaEnd.  Returns the number of stages begun; *abort is set
+// where a wait ran out.
+template <int STAGES, class Put>
+__device__ __forceinline__ int pa_produce(const PagedAttnParams& A, PaRing<STAGES>& T, const PaSeq* plan, int cta, int lane,
+                                          Put put) {
+  const PagedAttnArgs& a = A.a;
+  const PagedRows& P = a.p;
+  volatile int* abort = &T.abort;
+  const int lbr = min(P.lps, 6), br = 1 << lbr;  // positions of a box
+  // lane l sums the sequences [l k, (l + 1) k); the lane that holds the
+  // CTA's first slot finds its sequence
+  auto slots = [&](int nch) { return nch > 0 ? (long long)P.nkv * (nch + kPaUnit) : 0LL; };
+  const int k = (P.n_seqs + 31) / 32;
+  long long sum = 0;
+  for (int i = 0; i < k; ++i)
+    if (lane * k + i < P.n_seqs) sum += slots(plan[lane * k + i].nch);
+  long long inc = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += o;
+  }
+  const long long W = __shfl_sync(0xffffffffu, inc, 31);
+  // no more CTAs than slots: every CTA inside a cut unit has a part of it
+  const int G = (int)min((long long)gridDim.x, W);
+  const bool small = W < 1 << 22;  // 32-bit divisions do
+  auto div = [&](long long x, long long y) {
+    return small ? (long long)((unsigned)x / (unsigned)y) : x / y;
+  };
+  const long long w0 = cta < G ? div(cta * W, G) : W, w1 = cta < G ? div((cta + 1) * W, G) : W;
+  long long base = inc - sum;
+  int b = lane * k;
+  const bool mine = base <= w0 && w0 < inc;
+  if (mine)
+    while (base + slots(plan[b].nch) <= w0) base += slots(plan[b++].nch);
+  const unsigned who = __ballot_sync(0xffffffffu, mine);
+  const int src = who ? __ffs(who) - 1 : 0;
+  b = __shfl_sync(0xffffffffu, b, src);
+  base = __shfl_sync(0xffffffffu, base, src);
+  PaSeq s{};
+  if (w0 < w1) s = plan[b];
+  // the plan's memory becomes the ring's: its reads before the async writes
+  __syncwarp();
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+
+  const int lnb = 6 - lbr;  // log2 of a chunk's boxes
+  int st = 0;
+  // A stage: its description (written by lane 0) and its bytes; false: given up.
+  auto begin = [&]() {
+    const int sl = st % STAGES;
+    bool ok = true;
+    if (st >= STAGES)
+      ok = !*abort && pa_wait(&T.empty[sl], (uint32_t)(st / STAGES - 1) & 1u, A.wait_ns, abort);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) *abort = 1;
+    return ok;
+  };
+  bool live = true;
+  int kvh = s.nch > 0 ? (int)div(w0 - base, s.nch + kPaUnit) : 0;
+  // page cache: lane l holds box l & (boxes - 1) of chunk cj + (l >> lnb) of sequence cb
+  int cb = -1, cj = 0, crow = 0;
+  bool cload = false;
+  while (live) {
+    const int span = s.nch + kPaUnit;
+    const long long rs = base + (long long)kvh * span + kPaUnit, re = rs + s.nch;  // the unit's chunks
+    if (rs >= w1 || w0 >= w1) break;
+    const int j0 = rs >= w0 ? 0 : (int)(w0 - rs), j1 = (int)(min(re, w1) - rs);
+    int cf = 0, np = 1;
+    if (rs < w0 || re > w1) {
+      cf = (int)div((rs + 1) * G - 1, W);
+      np = (int)div(re * G - 1, W) - cf + 1;
+    }
+    for (int j = j0; j < j1; ++j) {
+      if (b != cb || j < cj || j >= cj + (32 >> lnb)) {
+        cb = b;
+        cj = j;
+        const int c = j + (lane >> lnb);
+        const int p0 = (c < s.np ? s.cp + c : s.cm + c - s.np) * kPaChunk + ((lane & ((1 << lnb) - 1)) << lbr);
+        cload = c < s.nch && pa_any(s.len, s.n, s.first, s.prefix, a.window, p0, p0 + br - 1);
+        if (cload) {
+          int page = P.table[(size_t)b * P.max_pages + (p0 >> P.lps)];
+          if (page < 0 || page >= P.n_pages) {
+            atomicCAS(P.err, 0, (int)MOE_ERR_INVALID_ARG);
+            page = 0;
+          }
+          crow = (page * P.nkv << P.lps) + (p0 & ((1 << P.lps) - 1));
+        }
+      }
+      live = begin();
+      if (!live) break;
+      const bool load = cload && (lane >> lnb) == j - cj;
+      const unsigned boxes = __ballot_sync(0xffffffffu, load);
+      const int pos0 = (j < s.np ? s.cp + j : s.cm + j - s.np) * kPaChunk, sp = pos0 + 16 * (lane & 3);
+      const unsigned any = __ballot_sync(0xffffffffu, pa_any(s.len, s.n, s.first, s.prefix, a.window, sp, sp + 15));
+      const unsigned all = __ballot_sync(0xffffffffu, pa_all(s.len, s.n, s.first, s.prefix, a.window, sp, sp + 15));
+      const int sl = st % STAGES;
+      if (lane == 0) {
+        PaDesc& d = T.desc[sl];
+        d.q0 = s.q0;
+        d.n = s.n;
+        d.len = s.len;
+        d.kvh = kvh;
+        d.pos0 = pos0;
+        d.first = s.first;
+        d.prefix = s.prefix;
+        d.flags = (j == j1 - 1 ? kPaLast : 0) | (int)(any & 15u) << kPaAny | (int)(all & 15u) << kPaAll;
+        d.cf = cf;
+        d.np = np;
+        d.slot = rs >= w0;
+        mbar_arrive(&T.told[sl]);
+        mbar_arrive_expect_tx(&T.full[sl], __popc(boxes) * (uint32_t)(br * 512));
+      }
+      __syncwarp();
+      if (load) put(sl, lane & ((1 << lnb) - 1), crow + (kvh << P.lps), &T.full[sl]);
+      ++st;
+    }
+    if (!live || re >= w1) break;
+    if (++kvh == P.nkv) {
+      base += (long long)P.nkv * span;
+      kvh = 0;
+      do s = pa_seq(a, ++b, nullptr);
+      while (s.nch == 0);
+    }
+  }
+  if (live && (live = begin())) {
+    if (lane == 0) {
+      T.desc[st % STAGES].flags = kPaEnd;
+      mbar_arrive(&T.told[st % STAGES]);
+      mbar_arrive(&T.full[st % STAGES]);
+    }
+    ++st;
+  }
+  __syncwarp();
+  return st;
+}
+
+// After a wait ran out: records it and waits for the ring's copies in flight
+// (one thread, when every warp has left the ring).
+template <int STAGES>
+__device__ __forceinline__ void pa_drain(PaRing<STAGES>& T, int st, int* err) {
+  atomicCAS(err, 0, (int)MOE_ERR_DEVICE_TIMEOUT);
+  for (int i = max(0, st - STAGES); i < st; ++i)
+    mbar_wait_drain(&T.full[i % STAGES], (uint32_t)(i / STAGES) & 1u, kPaDrainNs);
+}
+
+}  // namespace
+
+}  // namespace moe

@@ -1,0 +1,581 @@
+// paged_attn_tc.cu -- the paged attention for 33 to 64 query rows a KV head
+// (verify rows x heads of the KV head) on the 5th-generation tensor cores.
+//
+// Same work list, ring and join as paged_attn.cu (one CTA an SM, four 32 KB
+// stages).  With 64 rows the products are 256 multiply-adds a byte of keys
+// and values: mma.sync's rate, and the fragments' trips through registers,
+// bound the other form.  Here, per 64-position chunk:
+//   S [rows, 64]    = Q K^T     8 tcgen05.mma M128 N64  K16, Q and K K-major
+//   O [rows, 128]  += P V       8 tcgen05.mma M128 N128 K16 (P = hi + lo), V
+//                               N-major as it lies in the page
+// with S and O in tensor memory and Q, P, K and V in shared memory (128-byte
+// swizzle).  M is 128 although 64 rows are real.  For S, rows 64-127 are the
+// same queries again, so that the scores also lie in the tensor memory lanes
+// that the other two of an SM's four warp slots reach: thread (row, half)
+// owns 32 scores of a row, and maximum and sum need one exchange with one
+// other thread.  (64 scores a thread, on two of the four schedulers: 234 us
+// for two sequences of ~100,000 positions and 64 rows, TODO here, 349 by
+// mma.sync.)  For O, rows 64-127 read whatever follows P and end where nobody
+// looks.
+//
+// Two groups of four such warps take even and odd chunks, each with its own
+// S, P and O (so one group's softmax runs beside the other's products) and
+// its own running maximum m; O is only rescaled when the maximum grows by more
+// than 2^8 (p <= 256 then; the result is the same, sums and outputs being in
+// FP32).  At a segment's end the first group adds the two.
+//
+// Hidden positions: as in paged_attn.cu a slice with hidden positions is
+// looked over for infinite or NaN values, and such a slice is kept out of the
+// product and added element by element.
+#include "paged_attn.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kTcStages = 4;
+constexpr int kTcThreads = 384;
+constexpr int kTcP = 2 * 8192;   // a group's P: hi, lo [64 rows][64 positions] bf16
+constexpr int kTcQ = 2 * 16384;  // Q: [dim half][64 rows twice][64 dims] bf16
+constexpr int kTcCols = 512;     // tensor memory columns
+constexpr int kTcS = 0, kTcO = 128;  // S of group g at 64 g, O at 128 + 128 g
+constexpr float kTcLazy = 8.f;   // growth of the maximum (log2) that is let pass
+// Warps: 0-3 and 4-7 softmax of the even and odd chunks (a warp reads the
+// tensor memory lanes of its number mod 4), 8 producer, 9 products, 10, 11
+// rows of Q.
+constexpr int kTcProducer = 8, kTcMma = 9, kTcLoader = 10;
+constexpr int kTcReaders = 8 + 2 + 1;  // of a stage: softmax warps, Q warps, the products
+
+struct TcTable {
+  PaRing<kTcStages> ring;
+  uint64_t s_full[2];   // S of group g is there
+  uint64_t x_full[2];   // group g's four warps have left what the others need
+  uint64_t p_full[2];   // P of group g is there (and its S read)
+  uint64_t o_done[2];   // the product with P of group g is done
+  uint64_t q_full[2], q_empty[2];
+  uint64_t ml_full;     // the segment's m and l of all but the first two warps
+  uint64_t epi_done;    // the segment's outputs are out of tensor memory
+  uint64_t fin;
+  uint32_t tmem;
+  int pv[2];            // slices to multiply (bits 0-3); bit 4: O holds sums already
+  float top[2][2][64];  // [group][half][row] maximum of a chunk's scores
+  float m[64], l[2][2][64];
+  int has;              // the second group has sums
+};
+
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  // shared-memory matrix descriptor: start, leading and stride byte offsets
+  // (16-byte units), version 1, 128-byte swizzle
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 | 1ull << 46 |
+         2ull << 61;
+}
+// Instruction descriptor of kind::f16: FP32 sums of bf16 products, M 128.
+__host__ __device__ constexpr uint32_t tc_idesc(int n, bool b_mn_major) {
+  return 1u << 4 | 1u << 7 | 1u << 10 | (b_mn_major ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (128u >> 4) << 24;
+}
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 32 columns of this thread's lane.
+__device__ __forceinline__ void tc_ld32(uint32_t t, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(t)
+      : "memory");
+}
+__device__ __forceinline__ void tc_st32(uint32_t t, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(t),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Bits [lo, hi) of a 64-bit mask.
+__device__ __forceinline__ unsigned long long tc_bits(int lo, int hi) {
+  lo = max(lo, 0);
+  hi = min(hi, 64);
+  if (lo >= hi) return 0ull;
+  const unsigned long long up = hi == 64 ? ~0ull : (1ull << hi) - 1ull;
+  return up & ~((1ull << lo) - 1ull);
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_constant__ PagedAttnParams A, int rows) {
+  const PagedAttnArgs& a = A.a;
+  const PagedRows& P = a.p;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  unsigned char* s_p = smem;                   // [group][hi, lo]
+  unsigned char* s_q = smem + 2 * kTcP;        // [segment parity]
+  unsigned char* ring = s_q + 2 * kTcQ;
+  TcTable& T = *reinterpret_cast<TcTable*>(ring + kTcStages * kPaStageBytes);
+  PaSeq* plan = reinterpret_cast<PaSeq*>(ring);  // [n_seqs], in the ring before its first load
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
+
+  if (threadIdx.x == 0) {
+    T.ring.abort = 0;
+    for (int i = 0; i < kTcStages; ++i) {
+      mbar_init(&T.ring.full[i], 1);
+      mbar_init(&T.ring.empty[i], kTcReaders);
+      mbar_init(&T.ring.told[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&T.s_full[i], 1);
+      mbar_init(&T.x_full[i], 4);
+      mbar_init(&T.p_full[i], 4);
+      mbar_init(&T.o_done[i], 1);
+      mbar_init(&T.q_full[i], 2);
+      mbar_init(&T.q_empty[i], 1);
+    }
+    mbar_init(&T.ml_full, 6);
+    mbar_init(&T.epi_done, 2);
+    mbar_init(&T.fin, 1);
+    fence_mbar_init();
+    prefetch_tensormap(&A.km);
+    prefetch_tensormap(&A.vm);
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  if (warp == kTcMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&T.tmem)), "n"(kTcCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  if (threadIdx.x == 0) A.rec[cta * 2].np = A.rec[cta * 2 + 1].np = 0;  // no parts yet
+  for (int b = threadIdx.x; b < P.n_seqs; b += kTcThreads) plan[b] = pa_seq(a, b, cta == 0 ? P.err : nullptr);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = T.tmem;
+  volatile int* abort = &T.ring.abort;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return !*abort && pa_wait(bar, parity, A.wait_ns, abort); };
+  int issued = 0;  // stages of the producer
+
+  if (warp == kTcProducer) {
+    const uint64_t pol = policy_evict_first();
+    const int br = 1 << min(P.lps, 6);
+    issued = pa_produce(A, T.ring, plan, cta, lane, [&](int sl, int box, int row, uint64_t* bar) {
+      unsigned char* dst = ring + (size_t)sl * kPaStageBytes + box * (br * 128);  // [dim half][64 positions][64 dims]
+      tma_load_3d(dst, &A.km, 0, row, 0, bar, pol);
+      tma_load_3d(dst + kPaHalf / 2, &A.km, 0, row, 1, bar, pol);
+      tma_load_3d(dst + kPaHalf, &A.vm, 0, row, 0, bar, pol);
+      tma_load_3d(dst + kPaHalf + kPaHalf / 2, &A.vm, 0, row, 1, bar, pol);
+    });
+  } else if (warp == kTcMma) {
+    // ---------------------------------------------------------------- products
+    if (lane == 0) {
+      const uint32_t q0 = smem_addr(s_q), p0 = smem_addr(s_p), r0 = smem_addr(ring);
+      constexpr uint32_t is = tc_idesc(64, false), io = tc_idesc(128, true);
+      int seg = 0, prev_seg = 0, prev_sl = -1;
+      bool fresh = true;
+      // O += P V of the chunk before
+      auto multiply = [&](int st) {
+        const int g = st & 1;
+        if (!wait(&T.p_full[g], (uint32_t)(st >> 1) & 1u)) return false;
+        const int pv = *reinterpret_cast<volatile int*>(&T.pv[g]);
+        if ((pv & 15) && !(pv & 16) && prev_seg > 0 && !wait(&T.epi_done, (uint32_t)(prev_seg - 1) & 1u)) return false;
+        tc_fence_after();
+        const uint32_t p = p0 + g * kTcP, v = r0 + prev_sl * kPaStageBytes + kPaHalf, d = tmem + kTcO + 128 * g;
+        bool acc = pv & 16;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          if (!(pv >> ks & 1)) continue;
+          const uint64_t b = tc_desc(v + ks * 2048, 8192, 1024);
+          tc_mma(d, tc_desc(p + ks * 32, 16, 1024), b, io, acc);
+          tc_mma(d, tc_desc(p + 8192 + ks * 32, 16, 1024), b, io, true);
+          acc = true;
+        }
+        tc_commit(&T.ring.empty[prev_sl]);
+        tc_commit(&T.o_done[g]);
+        return true;
+      };
+      bool ok = true;
+      for (int st = 0; ok; ++st) {
+        const int sl = st % kTcStages, g = st & 1;
+        ok = wait(&T.ring.full[sl], (uint32_t)(st / kTcStages) & 1u);
+        if (!ok) break;
+        const int flags = *reinterpret_cast<volatile int*>(&T.ring.desc[sl].flags);
+        if (flags & kPaEnd) {
+          if (st > 0) ok = multiply(st - 1);
+          break;
+        }
+        if (fresh) ok = wait(&T.q_full[seg & 1], (uint32_t)(seg >> 1) & 1u);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t q = q0 + (seg & 1) * kTcQ, k = r0 + sl * kPaStageBytes;
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+          const uint32_t off = (ks & 3) * 32;
+          tc_mma(tmem + kTcS + 64 * g, tc_desc(q + (ks >> 2) * 16384 + off, 16, 1024),
+                 tc_desc(k + (ks >> 2) * 8192 + off, 16, 1024), is, ks > 0);
+        }
+        tc_commit(&T.s_full[g]);
+        if (flags & kPaLast) tc_commit(&T.q_empty[seg & 1]);
+        if (st > 0) ok = multiply(st - 1);
+        prev_sl = sl;
+        prev_seg = seg;
+        fresh = flags & kPaLast;
+        if (fresh) ++seg;
+      }
+      if (!ok) *abort = 1;
+      // every product has ended before the CTA frees its memory
+      tc_commit(&T.fin);
+      mbar_wait_drain(&T.fin, 0, kPaDrainNs);
+    }
+    __syncwarp();
+  } else if (warp >= kTcLoader) {
+    // ---------------------------------------------------------------- rows of Q
+    int seg = 0;
+    bool fresh = true, ok = true;
+    for (int st = 0;; ++st) {
+      const int sl = st % kTcStages;
+      ok = __all_sync(0xffffffffu, wait(&T.ring.told[sl], (uint32_t)(st / kTcStages) & 1u));
+      if (!ok) break;
+      const PaDesc& D = T.ring.desc[sl];
+      const int flags = D.flags;
+      if (flags & kPaEnd) break;
+      if (fresh) {
+        if (seg >= 2) ok = __all_sync(0xffffffffu, wait(&T.q_empty[seg & 1], (uint32_t)((seg >> 1) - 1) & 1u));
+        if (!ok) break;
+        const uint32_t q = smem_addr(s_q) + (seg & 1) * kTcQ;
+        const int nrow = D.n * a.group;
+        for (int u = (warp - kTcLoader) * 32 + lane; u < 64 * 16; u += 64) {
+          const int i = u >> 4, c = u & 15;
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (i < nrow) {
+            const int r = i / a.group, h = D.kvh * a.group + i - r * a.group;
+            v = *reinterpret_cast<const uint4*>(a.q + (D.q0 + r) * a.qs + h * 128 + 8 * c);
+          }
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(q + (c >> 3) * 16384 + w * 8192 + i * 128 +
+                                                                         (((c & 7) ^ (i & 7)) << 4)),
+                         "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                         : "memory");
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&T.q_full[seg & 1]);
+      }
+      fresh = flags & kPaLast;
+      if (fresh) ++seg;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&T.ring.empty[sl]);
+    }
+    if (!ok) *abort = 1;
+  } else {
+    // ---------------------------------------------------------------- softmax
+    const int g = warp >> 2, half = (warp >> 1) & 1, row = 32 * (warp & 1) + lane;  // 32 positions of a row
+    const uint32_t t_lane = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t t_s = tmem + t_lane + kTcS + 64 * g + 32 * half, t_o = tmem + t_lane + kTcO + 128 * g;
+    const uint32_t p_row = smem_addr(s_p) + g * kTcP + row * 128;
+    int seg = 0, own = 0, rp = 0;
+    uint32_t xpar = 0;
+    bool fresh = true, ok = true, has = false;
+    float m = -INFINITY, l = 0.f, slope = 0.f;
+    auto all = [&](bool x) { return __all_sync(0xffffffffu, x); };
+    // the group's four warps: what each wrote before is there for all after
+    auto exchange = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&T.x_full[g]);
+      const bool r = all(wait(&T.x_full[g], xpar));
+      xpar ^= 1u;
+      return r;
+    };
+    for (int st = 0;; ++st) {
+      const int sl = st % kTcStages;
+      ok = all(wait(&T.ring.told[sl], (uint32_t)(st / kTcStages) & 1u));
+      if (!ok) break;
+      const PaDesc& D = T.ring.desc[sl];
+      const int flags = D.flags;
+      if (flags & kPaEnd) break;
+      if (fresh) {
+        m = -INFINITY;
+        l = 0.f;
+        has = false;
+        rp = D.len;
+        if (row < D.n * a.group) {
+          const int r = row / a.group;
+          rp += r;
+          if (a.slopes) slope = a.slopes[D.kvh * a.group + row - r * a.group] * 1.4426950408889634f;
+        }
+      }
+      if ((st & 1) == g) {
+        // the scores of positions pos0 + 32 half + c
+        ok = all(wait(&T.s_full[g], (uint32_t)own & 1u));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sr[32];
+        tc_ld32(t_s, sr);
+        tc_wait_ld();
+        float s[32];
+        const int pos0 = D.pos0;
+        if (a.plain) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) s[c] = __uint_as_float(sr[c]) * a.scale_log2;
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            // tanh(z) = 1 - 2 / (e^2z + 1): off by an FP32 rounding of 1, an
+            // absolute error, which is what a score needs
+            const float q = __uint_as_float(sr[c]);
+            float x = q * a.scale_log2;
+            if (a.cap_log2 > 0.f) x = a.cap_log2 * (1.f - 2.f * rcp(ex2(q * a.cap_in) + 1.f));
+            s[c] = x + slope * (float)(pos0 + 32 * half + c - rp);
+          }
+        }
+        unsigned long long see = ~0ull;
+        const int any = flags >> kPaAny & 15, clear = flags >> kPaAll & 15;
+        if (clear != 15) {
+          const int lo = a.window > 0 ? max(D.first, rp - a.window + 1) : D.first;
+          see = tc_bits(lo - pos0, rp + 1 - pos0) | tc_bits(D.first - pos0, min(D.prefix, rp + 1) - pos0);
+          const uint32_t mine = (uint32_t)(see >> (32 * half));
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (!(mine >> c & 1u)) s[c] = -INFINITY;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 32; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+        T.top[g][half][row] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (!(ok = exchange())) break;
+        const float top = fmaxf(T.top[g][0][row], T.top[g][1][row]);
+        float scale = 1.f;
+        if (top > m && (m == -INFINITY || top - m > kTcLazy)) {
+          if (m != -INFINITY) scale = ex2(m - top);  // else the row's sums are zeros
+          m = top;
+          l *= scale;
+        }
+        const float ref = m == -INFINITY ? 0.f : m;  // nothing visible yet
+        float add[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          s[c] = ex2(s[c] - ref);
+          add[c & 3] += s[c];
+        }
+        l += (add[0] + add[1]) + (add[2] + add[3]);
+        // P's place (and O) is free when the product before has ended
+        if (own > 0) ok = all(wait(&T.o_done[g], (uint32_t)(own - 1) & 1u));
+        if (!ok) break;
+        tc_fence_after();
+        if (half == 0 && has && __any_sync(0xffffffffu, scale != 1.f)) {
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t o[32];
+            tc_ld32(t_o + c, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * scale);
+            tc_st32(t_o + c, o);
+          }
+          tc_wait_st();
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float x = s[8 * c + 2 * u], y = s[8 * c + 2 * u + 1];
+            hi[u] = pa_pack(x, y);
+            lo[u] = pa_pack(x - __uint_as_float(hi[u] << 16), y - __uint_as_float(hi[u] & 0xFFFF0000u));
+          }
+          const uint32_t at = p_row + (((4 * half + c) ^ (row & 7)) << 4);
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3])
+                       : "memory");
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + 8192), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3])
+                       : "memory");
+        }
+        int pv = any;
+        if (any & ~clear) {
+          // slices with hidden positions: infinite or NaN values among them?
+          // (a lane looks at positions lane and lane + 32)
+          ok = all(wait(&T.ring.full[sl], (uint32_t)(st / kTcStages) & 1u));
+          if (!ok) break;
+          const uint32_t v0 = smem_addr(ring + (size_t)sl * kPaStageBytes + kPaHalf);
+          int odd = 0;
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const int p = lane + 32 * w;
+            bool bad = false;
+            if ((any & ~clear) >> (p >> 4) & 1)
+#pragma unroll 4
+              for (int c = 0; c < 64; ++c)
+                bad |= __vcmpeq2(lds32(v0 + (c >> 5) * 8192 + p * 128 + ((c + p) & 31) * 4) & 0x7F807F80u, 0x7F807F80u) != 0u;
+            const unsigned b = __ballot_sync(0xffffffffu, bad);
+            odd |= ((b & 0xFFFFu) ? 1 : 0) << (2 * w) | ((b >> 16) ? 1 : 0) << (2 * w + 1);
+          }
+          if (odd) {
+            pv &= ~odd;
+            // (all four warps found the same) the other half of the rows' P
+            if (!(ok = exchange())) break;
+            // these tensor memory lanes may still be read for the segment before
+            if (!has && g == 1 && seg > 0) ok = all(wait(&T.epi_done, (uint32_t)(seg - 1) & 1u));
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; half == 0 && c < 128; c += 32) {
+              uint32_t o[32];
+              if (has) {
+                tc_ld32(t_o + c, o);
+                tc_wait_ld();
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = 0u;
+              }
+#pragma unroll 1
+              for (int p = 0; p < 64; ++p) {
+                if (!(odd >> (p >> 4) & 1) || !(see >> p & 1ull)) continue;
+                const uint32_t e = p_row + (((p >> 3) ^ (row & 7)) << 4) + 2 * (p & 7);
+                uint16_t hi, lo;
+                asm volatile("ld.shared.u16 %0, [%2];\n ld.shared.u16 %1, [%2 + 8192];" : "=h"(hi), "=h"(lo) : "r"(e));
+                const float w = bf16_bits_to_float(hi) + bf16_bits_to_float(lo);
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                  const int dim = c + i;
+                  const uint32_t v = lds32(v0 + (dim >> 6) * 8192 + p * 128 + ((((dim >> 3) & 7) ^ (p & 7)) << 4) + (dim & 7) * 2);
+                  o[i] = __float_as_uint(__uint_as_float(o[i]) + w * __uint_as_float(v << 16));
+                  o[i + 1] = __float_as_uint(__uint_as_float(o[i + 1]) + w * __uint_as_float(v & 0xFFFF0000u));
+                }
+              }
+              __syncwarp();
+              tc_st32(t_o + c, o);
+            }
+            tc_wait_st();
+            has = true;
+          }
+        }
+        if ((warp & 3) == 0 && lane == 0) *reinterpret_cast<volatile int*>(&T.pv[g]) = pv | (has ? 16 : 0);
+        has = has || pv != 0;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&T.p_full[g]);
+        ++own;
+      }
+      fresh = flags & kPaLast;
+      if (fresh && (g == 1 || half == 1)) {  // hand m and l over
+        if (seg > 0) ok = all(wait(&T.epi_done, (uint32_t)(seg - 1) & 1u));
+        if (!ok) break;
+        T.l[g][half][row] = l;
+        if (g == 1 && half == 0) {
+          T.m[row] = m;
+          if (row == 0) T.has = has;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&T.ml_full);
+      } else if (fresh) {
+        // ---------------------------------------------------------------- the segment's end
+        ok = all(wait(&T.ml_full, (uint32_t)seg & 1u));
+        const bool has1 = ok && T.has;
+        const int n1 = (st + 1) >> 1;  // the second group's chunks so far
+        if (ok && has) ok = all(wait(&T.o_done[0], (uint32_t)(own - 1) & 1u));
+        if (ok && has1) ok = all(wait(&T.o_done[1], (uint32_t)(n1 - 1) & 1u));
+        if (!ok) break;
+        tc_fence_after();
+        const float m1 = has1 ? T.m[row] : -INFINITY, l0 = l + T.l[0][1][row];
+        const float l1 = has1 ? T.l[1][0][row] + T.l[1][1][row] : 0.f;
+        const float M = fmaxf(m, m1);
+        const float f0 = m == -INFINITY ? 0.f : ex2(m - M), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
+        const float L = l0 * f0 + l1 * f1;
+        const bool whole = D.np == 1, live = row < D.n * a.group;
+        const int r = live ? row / a.group : 0, h = D.kvh * a.group + (live ? row - r * a.group : 0);
+        const size_t prow = (size_t)(cta * 2 + D.slot) * rows + row;
+        const float f = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+          float v[32];
+          uint32_t o[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+          if (has) {
+            tc_ld32(t_o + c, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * f0;
+          }
+          if (has1) {
+            tc_ld32(t_o + 128 + c, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(o[i]) * f1;
+          }
+          if (live && whole) {
+            uint4* out = reinterpret_cast<uint4*>(a.o + (D.q0 + r) * a.os + h * 128 + c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              out[i] = make_uint4(pa_pack(v[8 * i] * f, v[8 * i + 1] * f), pa_pack(v[8 * i + 2] * f, v[8 * i + 3] * f),
+                                  pa_pack(v[8 * i + 4] * f, v[8 * i + 5] * f), pa_pack(v[8 * i + 6] * f, v[8 * i + 7] * f));
+          } else if (live) {
+            float4* out = reinterpret_cast<float4*>(A.part_o + prow * 128 + c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) __stcg(out + i, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+          }
+        }
+        if (live && whole && a.lse)
+          a.lse[(size_t)(D.q0 + r) * a.nq + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+        if (live && !whole) __stcg(reinterpret_cast<float2*>(A.part_ml + 2 * prow), make_float2(M, L));
+        if (!whole && row == 0) A.rec[cta * 2 + D.slot] = {D.cf, D.np, D.q0, D.n, D.kvh};
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&T.epi_done);
+      }
+      if (fresh) ++seg;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&T.ring.empty[sl]);
+    }
+    if (!ok) *abort = 1;
+  }
+  tc_fence_before();
+  __syncthreads();  // every warp is done with the ring and the tensor memory
+  tc_fence_after();
+  if (warp == kTcMma)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTcCols));
+  if (warp == kTcProducer && *abort && lane == 0) pa_drain(T.ring, issued, P.err);
+}
+
+cudaError_t launch_paged_attention_tc(const PagedAttnParams& A, int rows, cudaStream_t s) {
+  constexpr int smem = 2 * kTcP + 2 * kTcQ + kTcStages * kPaStageBytes + (int)sizeof(TcTable);
+  static_assert(smem <= 227 * 1024, "one CTA an SM");
+  const cudaError_t e = prepare_kernel<k_paged_attn_tc>(smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(num_sms() < kPagedMaxCtas ? num_sms() : kPagedMaxCtas);
+  cfg.blockDim = dim3(kTcThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_paged_attn_tc, A, rows);
+}
+
+}  // namespace moe

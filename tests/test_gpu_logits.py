@@ -147,6 +147,19 @@ def test_long_history_of_one_token(M):
     check(M, torch.randn(2, 9000, generator=torch.Generator().manual_seed(1)), d)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_more_repeated_tokens_than_a_list_holds(M, dtype):
+    # every token of a row once and some thousands of them again, over long tiles (many rows)
+    R, V = 700, 14001
+    g = torch.Generator().manual_seed(3)
+    tokens = torch.cat([torch.randperm(V, generator=g), torch.randint(0, 9000, (5000,), generator=g)]).int()
+    begin = torch.tensor([(r * 37) % 3000 for r in range(R)], dtype=torch.int32)
+    end = torch.tensor([len(tokens) - (r % 11) * 900 for r in range(R)], dtype=torch.int32)
+    check(M, torch.randn(R, V, generator=g).to(dtype),
+          dict(tokens=tokens, begin=begin, end=end, repetition=torch.full((R,), 1.25),
+               frequency=torch.rand(R, generator=g)))
+
+
 def test_rows_past_the_tables_are_recorded(M):
     R, V = 3, 900
     x = torch.randn(R, V, generator=torch.Generator().manual_seed(1))
