@@ -1,7 +1,7 @@
 // paged_attn_tc.cu -- the paged attention for 33 to 64 query rows a KV head
 // (verify rows x heads of the KV head) on the 5th-generation tensor cores.
 //
-// Same work list, ring and join as paged_attn.cu (one CTA an SM, four 32 KB
+// Same work list, ring and join as paged_attn.cu (one CTA an SM, five 32 KB
 // stages).  With 64 rows the products are 256 multiply-adds a byte of keys
 // and values: mma.sync's rate, and the fragments' trips through registers,
 // bound the other form.  Here, per 64-position chunk:
@@ -33,29 +33,30 @@ namespace moe {
 
 namespace {
 
-constexpr int kTcStages = 4;
+constexpr int kTcStages = 5;
 constexpr int kTcThreads = 384;
 constexpr int kTcP = 2 * 8192;   // a group's P: hi, lo [64 rows][64 positions] bf16
 constexpr int kTcQ = 2 * 16384;  // Q: [dim half][64 rows twice][64 dims] bf16
 constexpr int kTcCols = 512;     // tensor memory columns
-constexpr int kTcS = 0, kTcO = 128;  // S of group g at 64 g, O at 128 + 128 g
+constexpr int kTcS = 0, kTcO = 256;  // S of chunk c at 64 (c mod 4), O of group g at 256 + 128 g
 constexpr float kTcLazy = 8.f;   // growth of the maximum (log2) that is let pass
 // Warps: 0-3 and 4-7 softmax of the even and odd chunks (a warp reads the
-// tensor memory lanes of its number mod 4), 8 producer, 9 products, 10, 11
+// tensor memory lanes of its number mod 4), 8 producer, 9 and 10 products (S;
+// O: one warp for both spent 870 of 2200 clocks a chunk between the two), 11
 // rows of Q.
-constexpr int kTcProducer = 8, kTcMma = 9, kTcLoader = 10;
-constexpr int kTcReaders = 8 + 2 + 1;  // of a stage: softmax warps, Q warps, the products
+constexpr int kTcProducer = 8, kTcMma = 9, kTcMmaO = 10, kTcLoader = 11;
+constexpr int kTcReaders = 8 + 1 + 1;  // of a stage: softmax warps, the Q warp, the products
 
 struct TcTable {
   PaRing<kTcStages> ring;
-  uint64_t s_full[2];   // S of group g is there
+  uint64_t s_full[4], s_empty[4];  // S of chunk c (mod 4) is there; is read
   uint64_t x_full[2];   // group g's four warps have left what the others need
-  uint64_t p_full[2];   // P of group g is there (and its S read)
+  uint64_t p_full[2];   // P of group g is there
   uint64_t o_done[2];   // the product with P of group g is done
-  uint64_t q_full[2], q_empty[2];
+  uint64_t q_full, q_empty;  // the segment's Q is there; its last product with it is done
   uint64_t ml_full;     // the segment's m and l of all but the first two warps
   uint64_t epi_done;    // the segment's outputs are out of tensor memory
-  uint64_t fin;
+  uint64_t fin[2];
   uint32_t tmem;
   int pv[2];            // slices to multiply (bits 0-3); bit 4: O holds sums already
   float top[2][2][64];  // [group][half][row] maximum of a chunk's scores
@@ -72,6 +73,12 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lbo, uint32_
 // Instruction descriptor of kind::f16: FP32 sums of bf16 products, M 128.
 __host__ __device__ constexpr uint32_t tc_idesc(int n, bool b_mn_major) {
   return 1u << 4 | 1u << 7 | 1u << 10 | (b_mn_major ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (128u >> 4) << 24;
+}
+// One thread of the (whole) warp, the same one every time.
+__device__ __forceinline__ bool tc_elect() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
 }
 __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
@@ -133,8 +140,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
   const PagedRows& P = a.p;
   extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* s_p = smem;                   // [group][hi, lo]
-  unsigned char* s_q = smem + 2 * kTcP;        // [segment parity]
-  unsigned char* ring = s_q + 2 * kTcQ;
+  unsigned char* s_q = smem + 2 * kTcP;
+  unsigned char* ring = s_q + kTcQ;
   TcTable& T = *reinterpret_cast<TcTable*>(ring + kTcStages * kPaStageBytes);
   PaSeq* plan = reinterpret_cast<PaSeq*>(ring);  // [n_seqs], in the ring before its first load
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
@@ -146,17 +153,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
       mbar_init(&T.ring.empty[i], kTcReaders);
       mbar_init(&T.ring.told[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&T.s_full[i], 1);
+      mbar_init(&T.s_empty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&T.x_full[i], 4);
       mbar_init(&T.p_full[i], 4);
       mbar_init(&T.o_done[i], 1);
-      mbar_init(&T.q_full[i], 2);
-      mbar_init(&T.q_empty[i], 1);
     }
+    mbar_init(&T.q_full, 1);
+    mbar_init(&T.q_empty, 1);
     mbar_init(&T.ml_full, 6);
     mbar_init(&T.epi_done, 2);
-    mbar_init(&T.fin, 1);
+    mbar_init(&T.fin[0], 1);
+    mbar_init(&T.fin[1], 1);
     fence_mbar_init();
     prefetch_tensormap(&A.km);
     prefetch_tensormap(&A.vm);
@@ -175,7 +186,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
   tc_fence_after();
   const uint32_t tmem = T.tmem;
   volatile int* abort = &T.ring.abort;
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return !*abort && pa_wait(bar, parity, A.wait_ns, abort); };
+  // the whole warp waits: true if every lane has seen the phase end
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    bool r = A.wait_ns != 0 && mbar_try_wait(bar, parity);
+    if (__all_sync(0xffffffffu, r)) return true;
+    if (!r) r = !*abort && pa_wait(bar, parity, A.wait_ns, abort);
+    return (bool)__all_sync(0xffffffffu, r);
+  };
   int issued = 0;  // stages of the producer
 
   if (warp == kTcProducer) {
@@ -188,66 +205,89 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
       tma_load_3d(dst + kPaHalf, &A.vm, 0, row, 0, bar, pol);
       tma_load_3d(dst + kPaHalf + kPaHalf / 2, &A.vm, 0, row, 1, bar, pol);
     });
-  } else if (warp == kTcMma) {
+  } else if (warp == kTcMma || warp == kTcMmaO) {
     // ---------------------------------------------------------------- products
-    if (lane == 0) {
-      const uint32_t q0 = smem_addr(s_q), p0 = smem_addr(s_p), r0 = smem_addr(ring);
-      constexpr uint32_t is = tc_idesc(64, false), io = tc_idesc(128, true);
-      int seg = 0, prev_seg = 0, prev_sl = -1;
-      bool fresh = true;
-      // O += P V of the chunk before
-      auto multiply = [&](int st) {
-        const int g = st & 1;
-        if (!wait(&T.p_full[g], (uint32_t)(st >> 1) & 1u)) return false;
-        const int pv = *reinterpret_cast<volatile int*>(&T.pv[g]);
-        if ((pv & 15) && !(pv & 16) && prev_seg > 0 && !wait(&T.epi_done, (uint32_t)(prev_seg - 1) & 1u)) return false;
-        tc_fence_after();
-        const uint32_t p = p0 + g * kTcP, v = r0 + prev_sl * kPaStageBytes + kPaHalf, d = tmem + kTcO + 128 * g;
-        bool acc = pv & 16;
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          if (!(pv >> ks & 1)) continue;
-          const uint64_t b = tc_desc(v + ks * 2048, 8192, 1024);
-          tc_mma(d, tc_desc(p + ks * 32, 16, 1024), b, io, acc);
-          tc_mma(d, tc_desc(p + 8192 + ks * 32, 16, 1024), b, io, true);
-          acc = true;
-        }
-        tc_commit(&T.ring.empty[prev_sl]);
-        tc_commit(&T.o_done[g]);
-        return true;
-      };
-      bool ok = true;
-      for (int st = 0; ok; ++st) {
-        const int sl = st % kTcStages, g = st & 1;
+    // The warp walks as one and elects a thread for each batch of products:
+    // their operands then stay in uniform registers (all by one thread of a
+    // diverged warp: 252 us against 199).
+    // (A descriptor's start address is its lowest bits, in 16-byte units: one
+    // add moves it.)
+    const uint64_t q0 = tc_desc(smem_addr(s_q), 16, 1024), p0 = tc_desc(smem_addr(s_p), 16, 1024);
+    const uint64_t k0 = tc_desc(smem_addr(ring), 16, 1024), v0 = tc_desc(smem_addr(ring) + kPaHalf, 8192, 1024);
+    constexpr uint32_t is = tc_idesc(64, false), io = tc_idesc(128, true);
+    int seg = 0;
+    bool fresh = true, ok = true;
+    if (warp == kTcMma) {
+      // S = Q K^T, up to four chunks ahead of what the softmax has read
+      for (int st = 0;; ++st) {
+        const int sl = st % kTcStages;
         ok = wait(&T.ring.full[sl], (uint32_t)(st / kTcStages) & 1u);
         if (!ok) break;
-        const int flags = *reinterpret_cast<volatile int*>(&T.ring.desc[sl].flags);
-        if (flags & kPaEnd) {
-          if (st > 0) ok = multiply(st - 1);
-          break;
-        }
-        if (fresh) ok = wait(&T.q_full[seg & 1], (uint32_t)(seg >> 1) & 1u);
+        const int flags = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&T.ring.desc[sl].flags), 0);
+        if (flags & kPaEnd) break;
+        if (fresh) ok = wait(&T.q_full, (uint32_t)seg & 1u);
+        if (ok && st > 3) ok = wait(&T.s_empty[st & 3], (uint32_t)((st >> 2) - 1) & 1u);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t q = q0 + (seg & 1) * kTcQ, k = r0 + sl * kPaStageBytes;
+        const uint64_t k = k0 + (unsigned)(sl * (kPaStageBytes >> 4));
+        if (tc_elect()) {
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          const uint32_t off = (ks & 3) * 32;
-          tc_mma(tmem + kTcS + 64 * g, tc_desc(q + (ks >> 2) * 16384 + off, 16, 1024),
-                 tc_desc(k + (ks >> 2) * 8192 + off, 16, 1024), is, ks > 0);
+          for (int ks = 0; ks < 8; ++ks)
+            tc_mma(tmem + kTcS + 64 * (st & 3), q0 + (ks >> 2) * 1024 + (ks & 3) * 2, k + (ks >> 2) * 512 + (ks & 3) * 2, is,
+                   ks > 0);
+          tc_commit(&T.s_full[st & 3]);
+          if (flags & kPaLast) tc_commit(&T.q_empty);
         }
-        tc_commit(&T.s_full[g]);
-        if (flags & kPaLast) tc_commit(&T.q_empty[seg & 1]);
-        if (st > 0) ok = multiply(st - 1);
-        prev_sl = sl;
-        prev_seg = seg;
+        __syncwarp();
         fresh = flags & kPaLast;
         if (fresh) ++seg;
       }
-      if (!ok) *abort = 1;
-      // every product has ended before the CTA frees its memory
-      tc_commit(&T.fin);
-      mbar_wait_drain(&T.fin, 0, kPaDrainNs);
+    } else {
+      // O += P V
+      for (int st = 0;; ++st) {
+        const int sl = st % kTcStages, g = st & 1;
+        ok = wait(&T.ring.told[sl], (uint32_t)(st / kTcStages) & 1u);
+        if (!ok) break;
+        const int flags = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&T.ring.desc[sl].flags), 0);
+        if (flags & kPaEnd) break;
+        ok = wait(&T.p_full[g], (uint32_t)(st >> 1) & 1u);
+        if (!ok) break;
+        const int pv = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&T.pv[g]), 0);
+        if ((pv & 15) && !(pv & 16) && seg > 0) ok = wait(&T.epi_done, (uint32_t)(seg - 1) & 1u);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t p = p0 + (unsigned)(g * (kTcP >> 4)), v = v0 + (unsigned)(sl * (kPaStageBytes >> 4));
+        const uint32_t d = tmem + kTcO + 128 * g;
+        if (tc_elect()) {
+          if ((pv & 15) == 15) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+              tc_mma(d, p + 2 * ks, v + 128 * ks, io, ks > 0 || (pv & 16));
+              tc_mma(d, p + 512 + 2 * ks, v + 128 * ks, io, true);
+            }
+          } else {
+            bool acc = pv & 16;
+#pragma unroll 1
+            for (int ks = 0; ks < 4; ++ks) {
+              if (!(pv >> ks & 1)) continue;
+              tc_mma(d, p + 2 * ks, v + 128 * ks, io, acc);
+              tc_mma(d, p + 512 + 2 * ks, v + 128 * ks, io, true);
+              acc = true;
+            }
+          }
+          tc_commit(&T.ring.empty[sl]);
+          tc_commit(&T.o_done[g]);
+        }
+        __syncwarp();
+        if (flags & kPaLast) ++seg;
+      }
+    }
+    if (!ok) *abort = 1;
+    // every product has ended before the CTA frees its memory
+    if (tc_elect()) {
+      uint64_t* fin = &T.fin[warp - kTcMma];
+      tc_commit(fin);
+      mbar_wait_drain(fin, 0, kPaDrainNs);
     }
     __syncwarp();
   } else if (warp >= kTcLoader) {
@@ -256,33 +296,40 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
     bool fresh = true, ok = true;
     for (int st = 0;; ++st) {
       const int sl = st % kTcStages;
-      ok = __all_sync(0xffffffffu, wait(&T.ring.told[sl], (uint32_t)(st / kTcStages) & 1u));
+      ok = wait(&T.ring.told[sl], (uint32_t)(st / kTcStages) & 1u);
       if (!ok) break;
       const PaDesc& D = T.ring.desc[sl];
       const int flags = D.flags;
       if (flags & kPaEnd) break;
       if (fresh) {
-        if (seg >= 2) ok = __all_sync(0xffffffffu, wait(&T.q_empty[seg & 1], (uint32_t)((seg >> 1) - 1) & 1u));
-        if (!ok) break;
-        const uint32_t q = smem_addr(s_q) + (seg & 1) * kTcQ;
-        const int nrow = D.n * a.group;
-        for (int u = (warp - kTcLoader) * 32 + lane; u < 64 * 16; u += 64) {
-          const int i = u >> 4, c = u & 15;
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        // the next segment's rows wait in registers until the last one's are done with
+        const uint32_t q = smem_addr(s_q);
+        const int nrow = D.n * a.group, c = lane & 15, i0 = lane >> 4;
+        uint4 v[32];
+#pragma unroll
+        for (int u = 0; u < 32; ++u) {
+          const int i = i0 + 2 * u;
+          v[u] = make_uint4(0u, 0u, 0u, 0u);
           if (i < nrow) {
             const int r = i / a.group, h = D.kvh * a.group + i - r * a.group;
-            v = *reinterpret_cast<const uint4*>(a.q + (D.q0 + r) * a.qs + h * 128 + 8 * c);
+            v[u] = *reinterpret_cast<const uint4*>(a.q + (D.q0 + r) * a.qs + h * 128 + 8 * c);
           }
+        }
+        if (seg > 0) ok = wait(&T.q_empty, (uint32_t)(seg - 1) & 1u);
+        if (!ok) break;
+#pragma unroll
+        for (int u = 0; u < 32; ++u) {
+          const int i = i0 + 2 * u;
 #pragma unroll
           for (int w = 0; w < 2; ++w)
             asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(q + (c >> 3) * 16384 + w * 8192 + i * 128 +
                                                                          (((c & 7) ^ (i & 7)) << 4)),
-                         "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                         "r"(v[u].x), "r"(v[u].y), "r"(v[u].z), "r"(v[u].w)
                          : "memory");
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(&T.q_full[seg & 1]);
+        if (lane == 0) mbar_arrive(&T.q_full);
       }
       fresh = flags & kPaLast;
       if (fresh) ++seg;
@@ -294,24 +341,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
     // ---------------------------------------------------------------- softmax
     const int g = warp >> 2, half = (warp >> 1) & 1, row = 32 * (warp & 1) + lane;  // 32 positions of a row
     const uint32_t t_lane = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t t_s = tmem + t_lane + kTcS + 64 * g + 32 * half, t_o = tmem + t_lane + kTcO + 128 * g;
+    const uint32_t t_s = tmem + t_lane + kTcS + 32 * half, t_o = tmem + t_lane + kTcO + 128 * g;
     const uint32_t p_row = smem_addr(s_p) + g * kTcP + row * 128;
     int seg = 0, own = 0, rp = 0;
     uint32_t xpar = 0;
     bool fresh = true, ok = true, has = false;
     float m = -INFINITY, l = 0.f, slope = 0.f;
-    auto all = [&](bool x) { return __all_sync(0xffffffffu, x); };
     // the group's four warps: what each wrote before is there for all after
     auto exchange = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(&T.x_full[g]);
-      const bool r = all(wait(&T.x_full[g], xpar));
+      const bool r = wait(&T.x_full[g], xpar);
       xpar ^= 1u;
       return r;
     };
     for (int st = 0;; ++st) {
       const int sl = st % kTcStages;
-      ok = all(wait(&T.ring.told[sl], (uint32_t)(st / kTcStages) & 1u));
+      ok = wait(&T.ring.told[sl], (uint32_t)(st / kTcStages) & 1u);
       if (!ok) break;
       const PaDesc& D = T.ring.desc[sl];
       const int flags = D.flags;
@@ -329,12 +375,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
       }
       if ((st & 1) == g) {
         // the scores of positions pos0 + 32 half + c
-        ok = all(wait(&T.s_full[g], (uint32_t)own & 1u));
+        ok = wait(&T.s_full[st & 3], (uint32_t)(st >> 2) & 1u);
         if (!ok) break;
         tc_fence_after();
         uint32_t sr[32];
-        tc_ld32(t_s, sr);
+        tc_ld32(t_s + 64 * (st & 3), sr);
         tc_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&T.s_empty[st & 3]);
         float s[32];
         const int pos0 = D.pos0;
         if (a.plain) {
@@ -382,7 +431,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
         }
         l += (add[0] + add[1]) + (add[2] + add[3]);
         // P's place (and O) is free when the product before has ended
-        if (own > 0) ok = all(wait(&T.o_done[g], (uint32_t)(own - 1) & 1u));
+        if (own > 0) ok = wait(&T.o_done[g], (uint32_t)(own - 1) & 1u);
         if (!ok) break;
         tc_fence_after();
         if (half == 0 && has && __any_sync(0xffffffffu, scale != 1.f)) {
@@ -416,7 +465,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
         if (any & ~clear) {
           // slices with hidden positions: infinite or NaN values among them?
           // (a lane looks at positions lane and lane + 32)
-          ok = all(wait(&T.ring.full[sl], (uint32_t)(st / kTcStages) & 1u));
+          ok = wait(&T.ring.full[sl], (uint32_t)(st / kTcStages) & 1u);
           if (!ok) break;
           const uint32_t v0 = smem_addr(ring + (size_t)sl * kPaStageBytes + kPaHalf);
           int odd = 0;
@@ -436,7 +485,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
             // (all four warps found the same) the other half of the rows' P
             if (!(ok = exchange())) break;
             // these tensor memory lanes may still be read for the segment before
-            if (!has && g == 1 && seg > 0) ok = all(wait(&T.epi_done, (uint32_t)(seg - 1) & 1u));
+            if (!has && g == 1 && seg > 0) ok = wait(&T.epi_done, (uint32_t)(seg - 1) & 1u);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
@@ -481,7 +530,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
       }
       fresh = flags & kPaLast;
       if (fresh && (g == 1 || half == 1)) {  // hand m and l over
-        if (seg > 0) ok = all(wait(&T.epi_done, (uint32_t)(seg - 1) & 1u));
+        if (seg > 0) ok = wait(&T.epi_done, (uint32_t)(seg - 1) & 1u);
         if (!ok) break;
         T.l[g][half][row] = l;
         if (g == 1 && half == 0) {
@@ -492,11 +541,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
         if (lane == 0) mbar_arrive(&T.ml_full);
       } else if (fresh) {
         // ---------------------------------------------------------------- the segment's end
-        ok = all(wait(&T.ml_full, (uint32_t)seg & 1u));
+        ok = wait(&T.ml_full, (uint32_t)seg & 1u);
         const bool has1 = ok && T.has;
         const int n1 = (st + 1) >> 1;  // the second group's chunks so far
-        if (ok && has) ok = all(wait(&T.o_done[0], (uint32_t)(own - 1) & 1u));
-        if (ok && has1) ok = all(wait(&T.o_done[1], (uint32_t)(n1 - 1) & 1u));
+        if (ok && has) ok = wait(&T.o_done[0], (uint32_t)(own - 1) & 1u);
+        if (ok && has1) ok = wait(&T.o_done[1], (uint32_t)(n1 - 1) & 1u);
         if (!ok) break;
         tc_fence_after();
         const float m1 = has1 ? T.m[row] : -INFINITY, l0 = l + T.l[0][1][row];
@@ -561,7 +610,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
 }
 
 cudaError_t launch_paged_attention_tc(const PagedAttnParams& A, int rows, cudaStream_t s) {
-  constexpr int smem = 2 * kTcP + 2 * kTcQ + kTcStages * kPaStageBytes + (int)sizeof(TcTable);
+  constexpr int smem = 2 * kTcP + kTcQ + kTcStages * kPaStageBytes + (int)sizeof(TcTable);
   static_assert(smem <= 227 * 1024, "one CTA an SM");
   const cudaError_t e = prepare_kernel<k_paged_attn_tc>(smem);
   if (e != cudaSuccess) return e;
