@@ -46,8 +46,22 @@ constexpr int kPaWarps = 8;                      // compute warps
 constexpr int kPaThreads = (kPaWarps + 1) * 32;  // and the producer
 constexpr int kPaStages = 3;
 
+// A chunk as its stage's readers see it.
+struct PaDesc {
+  int q0, n, len, kvh;       // the sequence's first row, rows, committed length; KV head
+  int pos0, first, prefix;   // the chunk's first position; the sequence's limits
+  int flags;                 // kPaLast: the segment's last chunk; kPaEnd; kPaAny, kPaAll
+  int cf, np;                // np > 1: a cut unit, whose first CTA is cf and whose parts are np
+  int slot, pad;             // where this CTA's part goes (0 / 1)
+};
+constexpr int kPaLast = 1, kPaEnd = 2;  // kPaEnd: no chunk, the CTA is done
+constexpr int kPaAny = 4, kPaAll = 8;   // bit of the first of four 16-position slices: some row sees
+                                        // some of it / every row sees all of it
+
 struct PaTable {
   PaRing<kPaStages> ring;
+  uint64_t told[kPaStages];  // the description is written (the data may still be on its way)
+  PaDesc desc[kPaStages];
   float m[kPaWarps * 16];  // [tile][row][part]: maxima of the parts' scores; at a segment's end their sums
 };
 
@@ -102,7 +116,7 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
     for (int i = 0; i < kPaStages; ++i) {
       mbar_init(&T.ring.full[i], 1);
       mbar_init(&T.ring.empty[i], kPaWarps);
-      mbar_init(&T.ring.told[i], 1);
+      mbar_init(&T.told[i], 1);
     }
     fence_mbar_init();
     prefetch_tensormap(&A.km);
@@ -116,13 +130,40 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
 
   volatile int* abort = &T.ring.abort;
   if (warp == kPaWarps) {
-    unsigned char* ring = smem;
-    const uint64_t pol = policy_evict_first();
-    const int st = pa_produce(A, T.ring, plan, cta, lane, [&](int sl, int box, int row, uint64_t* bar) {
-      unsigned char* dst = ring + (size_t)sl * kPaStageBytes + box * (br * 256);
-      tma_load_3d(dst, &A.km, 0, row, 0, bar, pol);
-      tma_load_3d(dst + kPaHalf, &A.vm, 0, row, 0, bar, pol);
-    });
+    struct Out {
+      const PagedAttnParams& A;
+      PaTable& T;
+      unsigned char* ring;
+      uint64_t pol;
+      int lane, br, window;
+      __device__ bool begin(const PaSegment&, int) { return true; }
+      __device__ void stage(const PaSegment& g, int j, int st, uint32_t bytes) {
+        const PaSeq& s = g.s;
+        const int pos0 = g.pos(j), sp = pos0 + 16 * (lane & 3), sl = st % kPaStages;
+        const unsigned any = __ballot_sync(0xffffffffu, pa_any(s.len, s.n, s.first, s.prefix, window, sp, sp + 15));
+        const unsigned all = __ballot_sync(0xffffffffu, pa_all(s.len, s.n, s.first, s.prefix, window, sp, sp + 15));
+        if (lane != 0) return;
+        T.desc[sl] = {s.q0, s.n, s.len, g.kvh, pos0, s.first, s.prefix,
+                      (j == g.j1 - 1 ? kPaLast : 0) | (int)(any & 15u) << kPaAny | (int)(all & 15u) << kPaAll,
+                      g.cf, g.np, g.slot, 0};
+        mbar_arrive(&T.told[sl]);
+        mbar_arrive_expect_tx(&T.ring.full[sl], bytes);
+      }
+      __device__ void put(int sl, int box, int row, uint64_t* bar) {
+        unsigned char* dst = ring + (size_t)sl * kPaStageBytes + box * (br * 256);
+        tma_load_3d(dst, &A.km, 0, row, 0, bar, pol);
+        tma_load_3d(dst + kPaHalf, &A.vm, 0, row, 0, bar, pol);
+      }
+      __device__ bool end(int st) {
+        if (lane == 0) {
+          T.desc[st % kPaStages].flags = kPaEnd;
+          mbar_arrive(&T.told[st % kPaStages]);
+          mbar_arrive(&T.ring.full[st % kPaStages]);
+        }
+        return true;
+      }
+    };
+    const int st = pa_produce(A, T.ring, plan, cta, lane, Out{A, T, smem, policy_evict_first(), lane, br, a.window});
     __syncthreads();  // every warp is done with the ring
     if (*abort && lane == 0) pa_drain(T.ring, st, P.err);
     return;
@@ -145,10 +186,10 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
   for (int st = 0;; ++st) {
     const int sl = st % kPaStages;
     const uint32_t par = (uint32_t)(st / kPaStages) & 1u;
-    const PaDesc& D = T.ring.desc[sl];
+    const PaDesc& D = T.desc[sl];
     bool ok = !*abort;
     if (fresh) {  // the rows are loaded while the keys are on their way
-      ok = ok && pa_wait(&T.ring.told[sl], par, A.wait_ns, abort);
+      ok = ok && pa_wait(&T.told[sl], par, A.wait_ns, abort);
       ok = __all_sync(0xffffffffu, ok);
       if (ok && !(D.flags & kPaEnd)) {
 #pragma unroll

@@ -15,24 +15,10 @@ constexpr int kPaStageBytes = 2 * kPaHalf;
 constexpr int kPaUnit = 1;                       // slots before a unit's chunks
 constexpr uint64_t kPaDrainNs = 2000000000ull;
 
-// A chunk as its stage's readers see it.
-struct PaDesc {
-  int q0, n, len, kvh;       // the sequence's first row, rows, committed length; KV head
-  int pos0, first, prefix;   // the chunk's first position; the sequence's limits
-  int flags;                 // kPaLast: the segment's last chunk; kPaEnd; kPaAny, kPaAll
-  int cf, np;                // np > 1: a cut unit, whose first CTA is cf and whose parts are np
-  int slot, pad;             // where this CTA's part goes (0 / 1)
-};
-constexpr int kPaLast = 1, kPaEnd = 2;  // kPaEnd: no chunk, the CTA is done
-constexpr int kPaAny = 4, kPaAll = 8;   // bit of the first of four 16-position slices: some row sees
-                                        // some of it / every row sees all of it
-
 template <int STAGES>
 struct PaRing {
   uint64_t full[STAGES];
   uint64_t empty[STAGES];
-  uint64_t told[STAGES];  // the description is written (the data may still be on its way)
-  PaDesc desc[STAGES];
   int abort;
 };
 
@@ -114,14 +100,26 @@ __device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity, uint64_t
   return mbar_wait_bounded(bar, parity, limit_ns, abort);
 }
 
+// A CTA's segment of a (sequence, KV head) unit: chunks [j0, j1) of it.
+struct PaSegment {
+  PaSeq s;
+  int kvh, j0, j1;
+  int cf, np;  // np > 1: a cut unit, whose first CTA is cf and whose parts are np
+  int slot;    // where this CTA's part goes (0 / 1)
+  __device__ __forceinline__ int pos(int j) const { return (j < s.np ? s.cp + j : s.cm + j - s.np) * kPaChunk; }
+};
+
 // The producer warp: the CTA's share of the call's slots (plan: every
-// sequence), chunk by chunk into the ring; put(stage, box, row, barrier)
-// loads the box of br cache rows from `row` on (keys and values).  Ends with
-// a stage that says kPaEnd.  Returns the number of stages begun; *abort is set
-// where a wait ran out.
-template <int STAGES, class Put>
+// sequence), chunk by chunk into the ring.
+//   out.begin(segment, stage): a segment begins with this stage (false: gave up)
+//   out.stage(segment, j, stage, bytes): one lane, before the loads of chunk j
+//   out.put(slot, box, row, barrier): loads a box's keys and values, the
+//     cache rows from `row` on
+//   out.end(stage): the CTA's work is written down
+// Returns the number of stages begun; *abort is set where a wait ran out.
+template <int STAGES, class Out>
 __device__ __forceinline__ int pa_produce(const PagedAttnParams& A, PaRing<STAGES>& T, const PaSeq* plan, int cta, int lane,
-                                          Put put) {
+                                          Out out) {
   const PagedAttnArgs& a = A.a;
   const PagedRows& P = a.p;
   volatile int* abort = &T.abort;
@@ -164,12 +162,11 @@ __device__ __forceinline__ int pa_produce(const PagedAttnParams& A, PaRing<STAGE
 
   const int lnb = 6 - lbr;  // log2 of a chunk's boxes
   int st = 0;
-  // A stage: its description (written by lane 0) and its bytes; false: given up.
+  // the next stage's place in the ring; false: given up
   auto begin = [&]() {
-    const int sl = st % STAGES;
     bool ok = true;
     if (st >= STAGES)
-      ok = !*abort && pa_wait(&T.empty[sl], (uint32_t)(st / STAGES - 1) & 1u, A.wait_ns, abort);
+      ok = !*abort && pa_wait(&T.empty[st % STAGES], (uint32_t)(st / STAGES - 1) & 1u, A.wait_ns, abort);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) *abort = 1;
     return ok;
@@ -183,18 +180,19 @@ __device__ __forceinline__ int pa_produce(const PagedAttnParams& A, PaRing<STAGE
     const int span = s.nch + kPaUnit;
     const long long rs = base + (long long)kvh * span + kPaUnit, re = rs + s.nch;  // the unit's chunks
     if (rs >= w1 || w0 >= w1) break;
-    const int j0 = rs >= w0 ? 0 : (int)(w0 - rs), j1 = (int)(min(re, w1) - rs);
-    int cf = 0, np = 1;
+    PaSegment g{s, kvh, rs >= w0 ? 0 : (int)(w0 - rs), (int)(min(re, w1) - rs), 0, 1, rs >= w0};
     if (rs < w0 || re > w1) {
-      cf = (int)div((rs + 1) * G - 1, W);
-      np = (int)div(re * G - 1, W) - cf + 1;
+      g.cf = (int)div((rs + 1) * G - 1, W);
+      g.np = (int)div(re * G - 1, W) - g.cf + 1;
     }
-    for (int j = j0; j < j1; ++j) {
+    live = out.begin(g, st);
+    if (!live) break;
+    for (int j = g.j0; j < g.j1; ++j) {
       if (b != cb || j < cj || j >= cj + (32 >> lnb)) {
         cb = b;
         cj = j;
         const int c = j + (lane >> lnb);
-        const int p0 = (c < s.np ? s.cp + c : s.cm + c - s.np) * kPaChunk + ((lane & ((1 << lnb) - 1)) << lbr);
+        const int p0 = g.pos(c) + ((lane & ((1 << lnb) - 1)) << lbr);
         cload = c < s.nch && pa_any(s.len, s.n, s.first, s.prefix, a.window, p0, p0 + br - 1);
         if (cload) {
           int page = P.table[(size_t)b * P.max_pages + (p0 >> P.lps)];
@@ -209,28 +207,9 @@ __device__ __forceinline__ int pa_produce(const PagedAttnParams& A, PaRing<STAGE
       if (!live) break;
       const bool load = cload && (lane >> lnb) == j - cj;
       const unsigned boxes = __ballot_sync(0xffffffffu, load);
-      const int pos0 = (j < s.np ? s.cp + j : s.cm + j - s.np) * kPaChunk, sp = pos0 + 16 * (lane & 3);
-      const unsigned any = __ballot_sync(0xffffffffu, pa_any(s.len, s.n, s.first, s.prefix, a.window, sp, sp + 15));
-      const unsigned all = __ballot_sync(0xffffffffu, pa_all(s.len, s.n, s.first, s.prefix, a.window, sp, sp + 15));
-      const int sl = st % STAGES;
-      if (lane == 0) {
-        PaDesc& d = T.desc[sl];
-        d.q0 = s.q0;
-        d.n = s.n;
-        d.len = s.len;
-        d.kvh = kvh;
-        d.pos0 = pos0;
-        d.first = s.first;
-        d.prefix = s.prefix;
-        d.flags = (j == j1 - 1 ? kPaLast : 0) | (int)(any & 15u) << kPaAny | (int)(all & 15u) << kPaAll;
-        d.cf = cf;
-        d.np = np;
-        d.slot = rs >= w0;
-        mbar_arrive(&T.told[sl]);
-        mbar_arrive_expect_tx(&T.full[sl], __popc(boxes) * (uint32_t)(br * 512));
-      }
+      out.stage(g, j, st, __popc(boxes) * (uint32_t)(br * 512));
       __syncwarp();
-      if (load) put(sl, lane & ((1 << lnb) - 1), crow + (kvh << P.lps), &T.full[sl]);
+      if (load) out.put(st % STAGES, lane & ((1 << lnb) - 1), crow + (kvh << P.lps), &T.full[st % STAGES]);
       ++st;
     }
     if (!live || re >= w1) break;
@@ -241,14 +220,7 @@ __device__ __forceinline__ int pa_produce(const PagedAttnParams& A, PaRing<STAGE
       while (s.nch == 0);
     }
   }
-  if (live && (live = begin())) {
-    if (lane == 0) {
-      T.desc[st % STAGES].flags = kPaEnd;
-      mbar_arrive(&T.told[st % STAGES]);
-      mbar_arrive(&T.full[st % STAGES]);
-    }
-    ++st;
-  }
+  if (live && begin() && out.end(st)) ++st;
   __syncwarp();
   return st;
 }

@@ -45,23 +45,36 @@ constexpr float kTcLazy = 8.f;   // growth of the maximum (log2) that is let pas
 // O: one warp for both spent 870 of 2200 clocks a chunk between the two), 11
 // rows of Q.
 constexpr int kTcProducer = 8, kTcMma = 9, kTcMmaO = 10, kTcLoader = 11;
-constexpr int kTcReaders = 8 + 1 + 1;  // of a stage: softmax warps, the Q warp, the products
+constexpr int kTcSegs = 4;       // segments described ahead
+constexpr int kTcReaders = 11;   // of a segment's description: every warp but the producer
+
+// A segment as the warps see it: chunks j0 .. j0 + count - 1 of its unit, in
+// the ring's stages st0, st0 + 1, ...
+struct TcSeg {
+  int q0, n, len, kvh, first, prefix;
+  int cp, np, cm;  // of PaSeq
+  int j0, count, st0;
+  int cf, parts, slot;
+};
 
 struct TcTable {
   PaRing<kTcStages> ring;
+  uint64_t told[kTcSegs], read[kTcSegs];  // the segment's description is written; is read by all
+  TcSeg seg[kTcSegs];
   uint64_t s_full[4], s_empty[4];  // S of chunk c (mod 4) is there; is read
   uint64_t x_full[2];   // group g's four warps have left what the others need
   uint64_t p_full[2];   // P of group g is there
   uint64_t o_done[2];   // the product with P of group g is done
   uint64_t q_full, q_empty;  // the segment's Q is there; its last product with it is done
-  uint64_t ml_full;     // the segment's m and l of all but the first two warps
+  uint64_t ml_full;     // the segment's m and l are there
   uint64_t epi_done;    // the segment's outputs are out of tensor memory
   uint64_t fin[2];
   uint32_t tmem;
   int pv[2];            // slices to multiply (bits 0-3); bit 4: O holds sums already
   float top[2][2][64];  // [group][half][row] maximum of a chunk's scores
-  float m[64], l[2][2][64];
-  int has;              // the second group has sums
+  int odd[2][4];        // [group][warp] slices where it saw infinite or NaN values
+  float m[2][64], l[2][64];
+  int has[2];           // the group has sums
 };
 
 __device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
@@ -150,8 +163,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
     T.ring.abort = 0;
     for (int i = 0; i < kTcStages; ++i) {
       mbar_init(&T.ring.full[i], 1);
-      mbar_init(&T.ring.empty[i], kTcReaders);
-      mbar_init(&T.ring.told[i], 1);
+      mbar_init(&T.ring.empty[i], 1);
+    }
+    for (int i = 0; i < kTcSegs; ++i) {
+      mbar_init(&T.told[i], 1);
+      mbar_init(&T.read[i], kTcReaders);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&T.s_full[i], 1);
@@ -164,8 +180,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
     }
     mbar_init(&T.q_full, 1);
     mbar_init(&T.q_empty, 1);
-    mbar_init(&T.ml_full, 6);
-    mbar_init(&T.epi_done, 2);
+    mbar_init(&T.ml_full, 4);
+    mbar_init(&T.epi_done, 4);
     mbar_init(&T.fin[0], 1);
     mbar_init(&T.fin[1], 1);
     fence_mbar_init();
@@ -193,18 +209,56 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
     if (!r) r = !*abort && pa_wait(bar, parity, A.wait_ns, abort);
     return (bool)__all_sync(0xffffffffu, r);
   };
+  // segment i's description; done with it
+  auto told = [&](int i) { return wait(&T.told[i % kTcSegs], (uint32_t)(i / kTcSegs) & 1u); };
+  auto done = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&T.read[i % kTcSegs]);
+  };
   int issued = 0;  // stages of the producer
 
   if (warp == kTcProducer) {
-    const uint64_t pol = policy_evict_first();
-    const int br = 1 << min(P.lps, 6);
-    issued = pa_produce(A, T.ring, plan, cta, lane, [&](int sl, int box, int row, uint64_t* bar) {
-      unsigned char* dst = ring + (size_t)sl * kPaStageBytes + box * (br * 128);  // [dim half][64 positions][64 dims]
-      tma_load_3d(dst, &A.km, 0, row, 0, bar, pol);
-      tma_load_3d(dst + kPaHalf / 2, &A.km, 0, row, 1, bar, pol);
-      tma_load_3d(dst + kPaHalf, &A.vm, 0, row, 0, bar, pol);
-      tma_load_3d(dst + kPaHalf + kPaHalf / 2, &A.vm, 0, row, 1, bar, pol);
-    });
+    struct Out {
+      const PagedAttnParams& A;
+      TcTable& T;
+      unsigned char* ring;
+      volatile int* abort;
+      uint64_t pol;
+      int lane, br, n;  // n: segments
+      __device__ bool tell(const TcSeg& t) {
+        bool ok = true;
+        if (n >= kTcSegs)
+          ok = !*abort && pa_wait(&T.read[n % kTcSegs], (uint32_t)(n / kTcSegs - 1) & 1u, A.wait_ns, abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) *abort = 1;
+        if (ok && lane == 0) {
+          T.seg[n % kTcSegs] = t;
+          mbar_arrive(&T.told[n % kTcSegs]);
+        }
+        ++n;
+        return ok;
+      }
+      __device__ bool begin(const PaSegment& g, int st) {
+        const PaSeq& s = g.s;
+        return tell({s.q0, s.n, s.len, g.kvh, s.first, s.prefix, s.cp, s.np, s.cm, g.j0, g.j1 - g.j0, st, g.cf, g.np, g.slot});
+      }
+      __device__ void stage(const PaSegment&, int, int st, uint32_t bytes) {
+        if (lane == 0) mbar_arrive_expect_tx(&T.ring.full[st % kTcStages], bytes);
+      }
+      __device__ void put(int sl, int box, int row, uint64_t* bar) {
+        unsigned char* dst = ring + (size_t)sl * kPaStageBytes + box * (br * 128);  // [dim half][64 positions][64 dims]
+        tma_load_3d(dst, &A.km, 0, row, 0, bar, pol);
+        tma_load_3d(dst + kPaHalf / 2, &A.km, 0, row, 1, bar, pol);
+        tma_load_3d(dst + kPaHalf, &A.vm, 0, row, 0, bar, pol);
+        tma_load_3d(dst + kPaHalf + kPaHalf / 2, &A.vm, 0, row, 1, bar, pol);
+      }
+      __device__ bool end(int) {
+        tell(TcSeg{});  // no chunks: the CTA is done
+        return false;
+      }
+    };
+    issued = pa_produce(A, T.ring, plan, cta, lane,
+                        Out{A, T, ring, abort, policy_evict_first(), lane, 1 << min(P.lps, 6), 0});
   } else if (warp == kTcMma || warp == kTcMmaO) {
     // ---------------------------------------------------------------- products
     // The warp walks as one and elects a thread for each batch of products:
@@ -215,72 +269,70 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
     const uint64_t q0 = tc_desc(smem_addr(s_q), 16, 1024), p0 = tc_desc(smem_addr(s_p), 16, 1024);
     const uint64_t k0 = tc_desc(smem_addr(ring), 16, 1024), v0 = tc_desc(smem_addr(ring) + kPaHalf, 8192, 1024);
     constexpr uint32_t is = tc_idesc(64, false), io = tc_idesc(128, true);
-    int seg = 0;
-    bool fresh = true, ok = true;
-    if (warp == kTcMma) {
-      // S = Q K^T, up to four chunks ahead of what the softmax has read
-      for (int st = 0;; ++st) {
-        const int sl = st % kTcStages;
-        ok = wait(&T.ring.full[sl], (uint32_t)(st / kTcStages) & 1u);
-        if (!ok) break;
-        const int flags = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&T.ring.desc[sl].flags), 0);
-        if (flags & kPaEnd) break;
-        if (fresh) ok = wait(&T.q_full, (uint32_t)seg & 1u);
-        if (ok && st > 3) ok = wait(&T.s_empty[st & 3], (uint32_t)((st >> 2) - 1) & 1u);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t k = k0 + (unsigned)(sl * (kPaStageBytes >> 4));
-        if (tc_elect()) {
+    bool ok = true;
+    for (int seg = 0;; ++seg) {
+      ok = told(seg);
+      if (!ok) break;
+      const int st0 = __shfl_sync(0xffffffffu, T.seg[seg % kTcSegs].st0, 0);
+      const int st1 = st0 + __shfl_sync(0xffffffffu, T.seg[seg % kTcSegs].count, 0);
+      if (st0 == st1) break;
+      done(seg);
+      if (warp == kTcMma) {
+        // S = Q K^T, up to four chunks ahead of what the softmax has read
+        ok = wait(&T.q_full, (uint32_t)seg & 1u);
+        for (int st = st0; ok && st < st1; ++st) {
+          const int sl = st % kTcStages;
+          ok = wait(&T.ring.full[sl], (uint32_t)(st / kTcStages) & 1u);
+          if (ok && st > 3) ok = wait(&T.s_empty[st & 3], (uint32_t)((st >> 2) - 1) & 1u);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t k = k0 + (unsigned)(sl * (kPaStageBytes >> 4));
+          if (tc_elect()) {
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            tc_mma(tmem + kTcS + 64 * (st & 3), q0 + (ks >> 2) * 1024 + (ks & 3) * 2, k + (ks >> 2) * 512 + (ks & 3) * 2, is,
-                   ks > 0);
-          tc_commit(&T.s_full[st & 3]);
-          if (flags & kPaLast) tc_commit(&T.q_empty);
-        }
-        __syncwarp();
-        fresh = flags & kPaLast;
-        if (fresh) ++seg;
-      }
-    } else {
-      // O += P V
-      for (int st = 0;; ++st) {
-        const int sl = st % kTcStages, g = st & 1;
-        ok = wait(&T.ring.told[sl], (uint32_t)(st / kTcStages) & 1u);
-        if (!ok) break;
-        const int flags = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&T.ring.desc[sl].flags), 0);
-        if (flags & kPaEnd) break;
-        ok = wait(&T.p_full[g], (uint32_t)(st >> 1) & 1u);
-        if (!ok) break;
-        const int pv = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&T.pv[g]), 0);
-        if ((pv & 15) && !(pv & 16) && seg > 0) ok = wait(&T.epi_done, (uint32_t)(seg - 1) & 1u);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t p = p0 + (unsigned)(g * (kTcP >> 4)), v = v0 + (unsigned)(sl * (kPaStageBytes >> 4));
-        const uint32_t d = tmem + kTcO + 128 * g;
-        if (tc_elect()) {
-          if ((pv & 15) == 15) {
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-              tc_mma(d, p + 2 * ks, v + 128 * ks, io, ks > 0 || (pv & 16));
-              tc_mma(d, p + 512 + 2 * ks, v + 128 * ks, io, true);
-            }
-          } else {
-            bool acc = pv & 16;
-#pragma unroll 1
-            for (int ks = 0; ks < 4; ++ks) {
-              if (!(pv >> ks & 1)) continue;
-              tc_mma(d, p + 2 * ks, v + 128 * ks, io, acc);
-              tc_mma(d, p + 512 + 2 * ks, v + 128 * ks, io, true);
-              acc = true;
-            }
+            for (int ks = 0; ks < 8; ++ks)
+              tc_mma(tmem + kTcS + 64 * (st & 3), q0 + (ks >> 2) * 1024 + (ks & 3) * 2, k + (ks >> 2) * 512 + (ks & 3) * 2,
+                     is, ks > 0);
+            tc_commit(&T.s_full[st & 3]);
+            if (st == st1 - 1) tc_commit(&T.q_empty);
           }
-          tc_commit(&T.ring.empty[sl]);
-          tc_commit(&T.o_done[g]);
+          __syncwarp();
         }
-        __syncwarp();
-        if (flags & kPaLast) ++seg;
+      } else {
+        // O += P V
+        for (int st = st0; st < st1; ++st) {
+          const int sl = st % kTcStages, g = st & 1;
+          ok = wait(&T.p_full[g], (uint32_t)(st >> 1) & 1u);
+          if (!ok) break;
+          const int pv = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&T.pv[g]), 0);
+          if ((pv & 15) && !(pv & 16) && seg > 0) ok = wait(&T.epi_done, (uint32_t)(seg - 1) & 1u);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t p = p0 + (unsigned)(g * (kTcP >> 4)), v = v0 + (unsigned)(sl * (kPaStageBytes >> 4));
+          const uint32_t d = tmem + kTcO + 128 * g;
+          if (tc_elect()) {
+            if ((pv & 15) == 15) {
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks) {
+                tc_mma(d, p + 2 * ks, v + 128 * ks, io, ks > 0 || (pv & 16));
+                tc_mma(d, p + 512 + 2 * ks, v + 128 * ks, io, true);
+              }
+            } else {
+              bool acc = pv & 16;
+#pragma unroll 1
+              for (int ks = 0; ks < 4; ++ks) {
+                if (!(pv >> ks & 1)) continue;
+                tc_mma(d, p + 2 * ks, v + 128 * ks, io, acc);
+                tc_mma(d, p + 512 + 2 * ks, v + 128 * ks, io, true);
+                acc = true;
+              }
+            }
+            tc_commit(&T.ring.empty[sl]);
+            tc_commit(&T.o_done[g]);
+          }
+          __syncwarp();
+        }
       }
+      if (!ok) break;
     }
     if (!ok) *abort = 1;
     // every product has ended before the CTA frees its memory
@@ -292,49 +344,41 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
     __syncwarp();
   } else if (warp >= kTcLoader) {
     // ---------------------------------------------------------------- rows of Q
-    int seg = 0;
-    bool fresh = true, ok = true;
-    for (int st = 0;; ++st) {
-      const int sl = st % kTcStages;
-      ok = wait(&T.ring.told[sl], (uint32_t)(st / kTcStages) & 1u);
+    const uint32_t q = smem_addr(s_q);
+    bool ok = true;
+    for (int seg = 0;; ++seg) {
+      ok = told(seg);
       if (!ok) break;
-      const PaDesc& D = T.ring.desc[sl];
-      const int flags = D.flags;
-      if (flags & kPaEnd) break;
-      if (fresh) {
-        // the next segment's rows wait in registers until the last one's are done with
-        const uint32_t q = smem_addr(s_q);
-        const int nrow = D.n * a.group, c = lane & 15, i0 = lane >> 4;
-        uint4 v[32];
+      const TcSeg& D = T.seg[seg % kTcSegs];
+      if (D.count == 0) break;
+      // the segment's rows wait in registers until the last one's are done with
+      const int nrow = D.n * a.group, c = lane & 15, i0 = lane >> 4;
+      uint4 v[32];
 #pragma unroll
-        for (int u = 0; u < 32; ++u) {
-          const int i = i0 + 2 * u;
-          v[u] = make_uint4(0u, 0u, 0u, 0u);
-          if (i < nrow) {
-            const int r = i / a.group, h = D.kvh * a.group + i - r * a.group;
-            v[u] = *reinterpret_cast<const uint4*>(a.q + (D.q0 + r) * a.qs + h * 128 + 8 * c);
-          }
+      for (int u = 0; u < 32; ++u) {
+        const int i = i0 + 2 * u;
+        v[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (i < nrow) {
+          const int r = i / a.group, h = D.kvh * a.group + i - r * a.group;
+          v[u] = *reinterpret_cast<const uint4*>(a.q + (D.q0 + r) * a.qs + h * 128 + 8 * c);
         }
-        if (seg > 0) ok = wait(&T.q_empty, (uint32_t)(seg - 1) & 1u);
-        if (!ok) break;
-#pragma unroll
-        for (int u = 0; u < 32; ++u) {
-          const int i = i0 + 2 * u;
-#pragma unroll
-          for (int w = 0; w < 2; ++w)
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(q + (c >> 3) * 16384 + w * 8192 + i * 128 +
-                                                                         (((c & 7) ^ (i & 7)) << 4)),
-                         "r"(v[u].x), "r"(v[u].y), "r"(v[u].z), "r"(v[u].w)
-                         : "memory");
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&T.q_full);
       }
-      fresh = flags & kPaLast;
-      if (fresh) ++seg;
+      done(seg);
+      if (seg > 0) ok = wait(&T.q_empty, (uint32_t)(seg - 1) & 1u);
+      if (!ok) break;
+#pragma unroll
+      for (int u = 0; u < 32; ++u) {
+        const int i = i0 + 2 * u;
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(q + (c >> 3) * 16384 + w * 8192 + i * 128 +
+                                                                       (((c & 7) ^ (i & 7)) << 4)),
+                       "r"(v[u].x), "r"(v[u].y), "r"(v[u].z), "r"(v[u].w)
+                       : "memory");
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(&T.ring.empty[sl]);
+      if (lane == 0) mbar_arrive(&T.q_full);
     }
     if (!ok) *abort = 1;
   } else {
@@ -343,10 +387,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
     const uint32_t t_lane = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t t_s = tmem + t_lane + kTcS + 32 * half, t_o = tmem + t_lane + kTcO + 128 * g;
     const uint32_t p_row = smem_addr(s_p) + g * kTcP + row * 128;
-    int seg = 0, own = 0, rp = 0;
     uint32_t xpar = 0;
-    bool fresh = true, ok = true, has = false;
-    float m = -INFINITY, l = 0.f, slope = 0.f;
+    bool ok = true;
     // the group's four warps: what each wrote before is there for all after
     auto exchange = [&]() {
       __syncwarp();
@@ -355,25 +397,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
       xpar ^= 1u;
       return r;
     };
-    for (int st = 0;; ++st) {
-      const int sl = st % kTcStages;
-      ok = wait(&T.ring.told[sl], (uint32_t)(st / kTcStages) & 1u);
+    for (int seg = 0;; ++seg) {
+      ok = told(seg);
       if (!ok) break;
-      const PaDesc& D = T.ring.desc[sl];
-      const int flags = D.flags;
-      if (flags & kPaEnd) break;
-      if (fresh) {
-        m = -INFINITY;
-        l = 0.f;
-        has = false;
-        rp = D.len;
-        if (row < D.n * a.group) {
-          const int r = row / a.group;
-          rp += r;
-          if (a.slopes) slope = a.slopes[D.kvh * a.group + row - r * a.group] * 1.4426950408889634f;
+      const TcSeg& D = T.seg[seg % kTcSegs];
+      const int st0 = D.st0, st1 = st0 + D.count;
+      if (st0 == st1) break;
+      float m = -INFINITY, l = 0.f, slope = 0.f;
+      bool has = false;
+      const bool live = row < D.n * a.group;
+      const int r = live ? row / a.group : 0, h = D.kvh * a.group + (live ? row - r * a.group : 0);
+      const int rp = D.len + r;  // the row's position
+      if (a.slopes) slope = a.slopes[h] * 1.4426950408889634f;
+      for (int st = st0 + ((st0 & 1) != g); st < st1; st += 2) {
+        const int sl = st % kTcStages, own = st >> 1;
+        const int j = D.j0 + st - st0, pos0 = (j < D.np ? D.cp + j : D.cm + j - D.np) * kPaChunk;
+        // which 16-position slices some row sees some of, every row all of
+        int any = 15, clear = 15;
+        if (!pa_all(D.len, D.n, D.first, D.prefix, a.window, pos0, pos0 + 63)) {
+          const int sp = pos0 + 16 * (lane & 3);
+          any = __ballot_sync(0xffffffffu, pa_any(D.len, D.n, D.first, D.prefix, a.window, sp, sp + 15)) & 15;
+          clear = __ballot_sync(0xffffffffu, pa_all(D.len, D.n, D.first, D.prefix, a.window, sp, sp + 15)) & 15;
         }
-      }
-      if ((st & 1) == g) {
         // the scores of positions pos0 + 32 half + c
         ok = wait(&T.s_full[st & 3], (uint32_t)(st >> 2) & 1u);
         if (!ok) break;
@@ -385,7 +430,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
         __syncwarp();
         if (lane == 0) mbar_arrive(&T.s_empty[st & 3]);
         float s[32];
-        const int pos0 = D.pos0;
         if (a.plain) {
 #pragma unroll
           for (int c = 0; c < 32; ++c) s[c] = __uint_as_float(sr[c]) * a.scale_log2;
@@ -401,7 +445,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
           }
         }
         unsigned long long see = ~0ull;
-        const int any = flags >> kPaAny & 15, clear = flags >> kPaAll & 15;
         if (clear != 15) {
           const int lo = a.window > 0 ? max(D.first, rp - a.window + 1) : D.first;
           see = tc_bits(lo - pos0, rp + 1 - pos0) | tc_bits(D.first - pos0, min(D.prefix, rp + 1) - pos0);
@@ -414,6 +457,31 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
 #pragma unroll
         for (int c = 0; c < 32; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
         T.top[g][half][row] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const uint32_t v0 = smem_addr(ring + (size_t)sl * kPaStageBytes + kPaHalf);
+        if (any & ~clear) {
+          // slices with hidden positions: infinite or NaN values among them?
+          // (each of the four warps a quarter of the slice's bytes)
+          ok = wait(&T.ring.full[sl], (uint32_t)(st / kTcStages) & 1u);
+          if (!ok) break;
+          int odd = 0;
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {
+            if (!((any & ~clear) >> ks & 1)) continue;
+            const uint32_t at = v0 + ((warp >> 1) & 1) * 8192 + ks * 2048 + (warp & 1) * 1024 + lane * 16;
+            bool bad = false;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              uint32_t w[4];
+              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                           : "r"(at + 512 * u));
+#pragma unroll
+              for (int i = 0; i < 4; ++i) bad |= __vcmpeq2(w[i] & 0x7F807F80u, 0x7F807F80u) != 0u;
+            }
+            odd |= __any_sync(0xffffffffu, bad) << ks;
+          }
+          if (lane == 0) T.odd[g][warp & 3] = odd;
+        }
         if (!(ok = exchange())) break;
         const float top = fmaxf(T.top[g][0][row], T.top[g][1][row]);
         float scale = 1.f;
@@ -463,29 +531,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
         }
         int pv = any;
         if (any & ~clear) {
-          // slices with hidden positions: infinite or NaN values among them?
-          // (a lane looks at positions lane and lane + 32)
-          ok = wait(&T.ring.full[sl], (uint32_t)(st / kTcStages) & 1u);
-          if (!ok) break;
-          const uint32_t v0 = smem_addr(ring + (size_t)sl * kPaStageBytes + kPaHalf);
-          int odd = 0;
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const int p = lane + 32 * w;
-            bool bad = false;
-            if ((any & ~clear) >> (p >> 4) & 1)
-#pragma unroll 4
-              for (int c = 0; c < 64; ++c)
-                bad |= __vcmpeq2(lds32(v0 + (c >> 5) * 8192 + p * 128 + ((c + p) & 31) * 4) & 0x7F807F80u, 0x7F807F80u) != 0u;
-            const unsigned b = __ballot_sync(0xffffffffu, bad);
-            odd |= ((b & 0xFFFFu) ? 1 : 0) << (2 * w) | ((b >> 16) ? 1 : 0) << (2 * w + 1);
-          }
+          const int odd = T.odd[g][0] | T.odd[g][1] | T.odd[g][2] | T.odd[g][3];
           if (odd) {
             pv &= ~odd;
-            // (all four warps found the same) the other half of the rows' P
+            // (the same for all four warps) the other half of the rows' P
             if (!(ok = exchange())) break;
             // these tensor memory lanes may still be read for the segment before
-            if (!has && g == 1 && seg > 0) ok = wait(&T.epi_done, (uint32_t)(seg - 1) & 1u);
+            if (!has && seg > 0) ok = wait(&T.epi_done, (uint32_t)(seg - 1) & 1u);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
@@ -526,78 +578,72 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&T.p_full[g]);
-        ++own;
       }
-      fresh = flags & kPaLast;
-      if (fresh && (g == 1 || half == 1)) {  // hand m and l over
+      if (!ok) break;
+      {
+        // ---------------------------------------------------------------- the segment's end
+        // The second half's l joins the first's, and the groups hand theirs
+        // over; then the two groups' first warps add both groups' sums, the
+        // one's 64 dims and the other's.
         if (seg > 0) ok = wait(&T.epi_done, (uint32_t)(seg - 1) & 1u);
         if (!ok) break;
-        T.l[g][half][row] = l;
-        if (g == 1 && half == 0) {
-          T.m[row] = m;
-          if (row == 0) T.has = has;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&T.ml_full);
-      } else if (fresh) {
-        // ---------------------------------------------------------------- the segment's end
-        ok = wait(&T.ml_full, (uint32_t)seg & 1u);
-        const bool has1 = ok && T.has;
-        const int n1 = (st + 1) >> 1;  // the second group's chunks so far
-        if (ok && has) ok = wait(&T.o_done[0], (uint32_t)(own - 1) & 1u);
-        if (ok && has1) ok = wait(&T.o_done[1], (uint32_t)(n1 - 1) & 1u);
-        if (!ok) break;
-        tc_fence_after();
-        const float m1 = has1 ? T.m[row] : -INFINITY, l0 = l + T.l[0][1][row];
-        const float l1 = has1 ? T.l[1][0][row] + T.l[1][1][row] : 0.f;
-        const float M = fmaxf(m, m1);
-        const float f0 = m == -INFINITY ? 0.f : ex2(m - M), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
-        const float L = l0 * f0 + l1 * f1;
-        const bool whole = D.np == 1, live = row < D.n * a.group;
-        const int r = live ? row / a.group : 0, h = D.kvh * a.group + (live ? row - r * a.group : 0);
-        const size_t prow = (size_t)(cta * 2 + D.slot) * rows + row;
-        const float f = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
+        if (half == 1) T.l[g][row] = l;
+        if (!(ok = exchange())) break;
+        if (half == 0) {
+          T.l[g][row] += l;
+          T.m[g][row] = m;
+          if (row == 0) T.has[g] = has;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&T.ml_full);
+          const int n0 = (st1 + 1) >> 1, n1 = st1 >> 1;  // the groups' chunks so far
+          ok = wait(&T.ml_full, (uint32_t)seg & 1u);
+          const bool has0 = ok && T.has[0], has1 = ok && T.has[1];
+          if (ok && has0) ok = wait(&T.o_done[0], (uint32_t)(n0 - 1) & 1u);
+          if (ok && has1) ok = wait(&T.o_done[1], (uint32_t)(n1 - 1) & 1u);
+          if (!ok) break;
+          tc_fence_after();
+          const float m0 = has0 ? T.m[0][row] : -INFINITY, m1 = has1 ? T.m[1][row] : -INFINITY, M = fmaxf(m0, m1);
+          const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - M), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
+          const float L = (has0 ? T.l[0][row] : 0.f) * f0 + (has1 ? T.l[1][row] : 0.f) * f1;
+          const bool whole = D.parts == 1;
+          const size_t prow = (size_t)(cta * 2 + D.slot) * rows + row;
+          const float f = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
 #pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
-          float v[32];
-          uint32_t o[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0.f;
-          if (has) {
-            tc_ld32(t_o + c, o);
+          for (int c = 64 * g; c < 64 * g + 64; c += 32) {
+            uint32_t o0[32], o1[32];
+            float v[32];
+            if (has0) tc_ld32(tmem + t_lane + kTcO + c, o0);
+            if (has1) tc_ld32(tmem + t_lane + kTcO + 128 + c, o1);
             tc_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * f0;
+            for (int i = 0; i < 32; ++i) {
+              v[i] = has0 ? __uint_as_float(o0[i]) * f0 : 0.f;
+              if (has1) v[i] += __uint_as_float(o1[i]) * f1;
+            }
+            if (live && whole) {
+              uint4* out = reinterpret_cast<uint4*>(a.o + (D.q0 + r) * a.os + h * 128 + c);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                out[i] = make_uint4(pa_pack(v[8 * i] * f, v[8 * i + 1] * f), pa_pack(v[8 * i + 2] * f, v[8 * i + 3] * f),
+                                    pa_pack(v[8 * i + 4] * f, v[8 * i + 5] * f), pa_pack(v[8 * i + 6] * f, v[8 * i + 7] * f));
+            } else if (live) {
+              float4* out = reinterpret_cast<float4*>(A.part_o + prow * 128 + c);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) __stcg(out + i, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+            }
           }
-          if (has1) {
-            tc_ld32(t_o + 128 + c, o);
-            tc_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(o[i]) * f1;
-          }
-          if (live && whole) {
-            uint4* out = reinterpret_cast<uint4*>(a.o + (D.q0 + r) * a.os + h * 128 + c);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              out[i] = make_uint4(pa_pack(v[8 * i] * f, v[8 * i + 1] * f), pa_pack(v[8 * i + 2] * f, v[8 * i + 3] * f),
-                                  pa_pack(v[8 * i + 4] * f, v[8 * i + 5] * f), pa_pack(v[8 * i + 6] * f, v[8 * i + 7] * f));
-          } else if (live) {
-            float4* out = reinterpret_cast<float4*>(A.part_o + prow * 128 + c);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) __stcg(out + i, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&T.epi_done);
+          if (g == 0) {
+            if (live && whole && a.lse)
+              a.lse[(size_t)(D.q0 + r) * a.nq + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+            if (live && !whole) __stcg(reinterpret_cast<float2*>(A.part_ml + 2 * prow), make_float2(M, L));
+            if (!whole && row == 0) A.rec[cta * 2 + D.slot] = {D.cf, D.parts, D.q0, D.n, D.kvh};
           }
         }
-        if (live && whole && a.lse)
-          a.lse[(size_t)(D.q0 + r) * a.nq + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-        if (live && !whole) __stcg(reinterpret_cast<float2*>(A.part_ml + 2 * prow), make_float2(M, L));
-        if (!whole && row == 0) A.rec[cta * 2 + D.slot] = {D.cf, D.np, D.q0, D.n, D.kvh};
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&T.epi_done);
       }
-      if (fresh) ++seg;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&T.ring.empty[sl]);
+      done(seg);
     }
     if (!ok) *abort = 1;
   }
