@@ -38,57 +38,79 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return d;
 }
 
-__device__ __forceinline__ float unpack(const uint4& v, int i) {
-  const uint32_t w = i < 4 ? (i < 2 ? v.x : v.y) : (i < 6 ? v.z : v.w);
-  return (i & 1) ? __uint_as_float(w & 0xFFFF0000u) : __uint_as_float(w << 16);
+// Two floats, and two correctly rounded operations at a time.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 make_f2(float x, float y) {
+  f2 p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+  return p;
 }
+__device__ __forceinline__ f2 unpack2(uint32_t w) { return make_f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+__device__ __forceinline__ uint32_t pack2(f2 p) {
+  float x, y;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
+  return pack2(x, y);
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t& word(uint4& v, int i) { return reinterpret_cast<uint32_t*>(&v)[i]; }
 
 }  // namespace
 
 // CTA j: rows [rows j, rows (j + 1)).  The CTA copies the row starts, finds
 // its rows' sequences and slots, takes the angles' sines and cosines (thread
-// per pair), then walks its rows' heads, 16 lanes a head, 16 bytes a lane,
-// four heads in flight; the first four are loaded before anything else is
-// known, and a lane's sines and cosines are read once a row (one head at a
-// time, its angles element by element: 74 us against 55 for 8061 rows of 64
-// heads).
-// VEC: rd / 2 is a multiple of 8, so a piece's partner is one whole piece of
-// the same head (a shuffle); else each element's partner is loaded.
+// per pair), then walks its rows' heads.
+// VEC (rd / 2 a multiple of 8): eight lanes a head, each with two 16-byte
+// pieces.  The first rd / 16 lanes have a piece of the first half of the
+// rotary dims and its partner in the second, so a pair's four products need no
+// other lane and its sines and cosines serve both; the other lanes pass two
+// pieces on.  Two heads a lane are in flight, the first two from before
+// anything else is known.  The arithmetic is 3 instructions an element (one
+// piece a lane, its partner by shuffles, one float at a time: 12, which bound
+// the kernel: 74 us against 56 for 8061 rows of 64 heads).
+// Else: 16 lanes a head, each element's partner loaded.
 template <bool VEC>
 __global__ void __launch_bounds__(kApThreads) k_paged_append(const __grid_constant__ PagedAppendArgs a) {
-  constexpr int U = 4;
+  constexpr int U = 2;
   __shared__ int s_start[kPagedMaxSeqs + 1];
   __shared__ int s_pos[kApRows];
   __shared__ long long s_slot[kApRows];  // element of head 0, dim 0 of the row's slot, or -1
-  __shared__ float s_cos[kApRows][64], s_sin[kApRows][64];
+  __shared__ __align__(16) float s_cos[kApRows][64], s_sin[kApRows][64];
   const PagedRows& P = a.p;
   const int t0 = blockIdx.x * a.rows, ps = 1 << P.lps;
-  const int nqu = a.q ? a.nq : 0, units = nqu + 2 * P.nkv;
-  const int lane16 = threadIdx.x & 15, d0 = 8 * lane16, h0 = threadIdx.x >> 4;
-  constexpr int HS = kApThreads / 16;  // heads side by side
-  // this thread's piece of head u0 + k HS + h0: where it is read at row t0
-  const uint16_t* src[U];
-  uint4 x[U];
-  auto place = [&](int u0) {
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int u = u0 + k * HS + h0;
-      src[k] = (u < nqu ? a.q + t0 * a.qs + u * 128
-                : u < nqu + P.nkv ? a.k + t0 * a.ks + (u - nqu) * 128 : a.v + t0 * a.vs + (u - nqu - P.nkv) * 128) + d0;
-    }
+  const int nqu = a.q ? a.nq : 0, units = nqu + 2 * P.nkv, half = a.rd >> 1;
+  // VEC: this lane's pieces of a head, and whether they turn
+  constexpr int HS = kApThreads / (VEC ? 8 : 16);  // heads side by side
+  const int hl = half >> 3, l8 = threadIdx.x & 7, h0 = threadIdx.x / (VEC ? 8 : 16);
+  const bool turns = VEC && l8 < hl;
+  const int d0 = 8 * (turns ? l8 : 2 * l8), d1 = turns ? d0 + half : d0 + 8;
+  auto source = [&](int t, int u) {
+    return u < nqu ? a.q + t * a.qs + u * 128
+           : u < nqu + P.nkv ? a.k + t * a.ks + (u - nqu) * 128 : a.v + t * a.vs + (u - nqu - P.nkv) * 128;
   };
+  uint4 x[U], y[U];
   auto load = [&](int t, int u0) {
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       const int u = u0 + k * HS + h0;
-      x[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (t < P.T && u < units) x[k] = *reinterpret_cast<const uint4*>(src[k]);
+      if (t >= P.T || u >= units) continue;
+      const uint16_t* src = source(t, u);
+      x[k] = *reinterpret_cast<const uint4*>(src + d0);
+      y[k] = *reinterpret_cast<const uint4*>(src + d1);
     }
   };
   pdl_wait();
   pdl_launch_dependents();
-  place(0);
-  load(t0, 0);
+  if (VEC) load(t0, 0);
   for (int i = threadIdx.x; i <= P.n_seqs; i += kApThreads) s_start[i] = P.start[i];
   __syncthreads();
   if (threadIdx.x < a.rows) {
@@ -116,84 +138,82 @@ __global__ void __launch_bounds__(kApThreads) k_paged_append(const __grid_consta
     s_slot[threadIdx.x] = slot;
   }
   __syncthreads();
-  const int half = a.rd >> 1;
   for (int i = threadIdx.x; i < a.rows * half; i += kApThreads) {
     const int r = i / half, j = i - r * half;
     if (s_pos[r] >= 0) rope_cs(s_pos[r], a.freq[j], s_cos[r][j], s_sin[r][j]);
   }
   __syncthreads();
-  // the lane's eight angles: dims d0 .. d0 + 7 are pairs j0 .. j0 + 7, with
-  // the sine's sign by the half they lie in (VEC: a lane is in one half)
-  const int j0 = d0 < half ? d0 : d0 - half;
-  const bool turns = VEC && d0 < a.rd;
-  for (int u0 = 0; u0 < units; u0 += U * HS) {
-    if (u0 > 0) place(u0);
-    for (int r = 0; r < a.rows; ++r) {
-      const int t = t0 + r;
-      if (s_pos[r] >= 0) {  // else no sequence's row
-        if (r > 0 || u0 > 0) load(t, u0);
-        const long long slot = s_slot[r];
-        float c8[8], s8[8];
-        if (turns) {
+  for (int r = 0; r < a.rows; ++r) {
+    const int t = t0 + r;
+    if (s_pos[r] < 0) continue;  // no sequence's row
+    const long long slot = s_slot[r];
+    auto target = [&](int u) {
+      const bool isk = u < nqu + P.nkv;
+      return u < nqu ? a.qo + t * a.qos + u * 128
+             : slot >= 0 ? (isk ? P.kp : P.vp) + slot + ((long long)(u - nqu - (isk ? 0 : P.nkv)) << P.lps) * 128 : nullptr;
+    };
+    if constexpr (VEC) {
+      f2 c2[4], s2[4], n2[4];  // cosines, sines, minus the sines of dims d0 .. d0 + 7
+      if (turns) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            c8[i] = s_cos[r][j0 + i];
-            s8[i] = d0 < half ? -s_sin[r][j0 + i] : s_sin[r][j0 + i];
-          }
+        for (int i = 0; i < 4; ++i) {
+          const float2 c = *reinterpret_cast<const float2*>(&s_cos[r][d0 + 2 * i]);
+          const float2 s = *reinterpret_cast<const float2*>(&s_sin[r][d0 + 2 * i]);
+          c2[i] = make_f2(c.x, c.y);
+          s2[i] = make_f2(s.x, s.y);
+          n2[i] = make_f2(-s.x, -s.y);
         }
+      }
+      for (int u0 = 0; u0 < units; u0 += U * HS) {
+        if (r > 0 || u0 > 0) load(t, u0);
 #pragma unroll
         for (int k = 0; k < U; ++k) {
           const int u = u0 + k * HS + h0;
-          const bool isq = u < nqu, isk = !isq && u < nqu + P.nkv, live = u < units;
-          if (VEC) {
-            const int hl = half >> 3;  // lanes of half the rotary width
-            const int from = (threadIdx.x & 16) | (lane16 < hl ? lane16 + hl : lane16 < 2 * hl ? lane16 - hl : lane16);
-            uint4 o;
-            o.x = __shfl_sync(0xffffffffu, x[k].x, from);
-            o.y = __shfl_sync(0xffffffffu, x[k].y, from);
-            o.z = __shfl_sync(0xffffffffu, x[k].z, from);
-            o.w = __shfl_sync(0xffffffffu, x[k].w, from);
-            if (turns && (isq || isk)) {
-              float z[8];
+          if (u >= units) continue;
+          if (turns && u < nqu + P.nkv) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                z[i] = __fadd_rn(__fmul_rn(unpack(x[k], i), c8[i]), __fmul_rn(unpack(o, i), s8[i]));
-              x[k] = make_uint4(pack2(z[0], z[1]), pack2(z[2], z[3]), pack2(z[4], z[5]), pack2(z[6], z[7]));
-            }
-          } else {
-            const bool turn = live && (isq || isk) && d0 < a.rd;
-            float y[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int d = d0 + i;
-              y[i] = turn && d < a.rd ? bf16_bits_to_float(src[k][d < half ? i + half : i - half]) : 0.f;
-            }
-            __syncwarp();  // q_out may be q: every lane has read its head
-            if (turn) {
-              float z[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int d = d0 + i, j = d < half ? d : d - half;
-                z[i] = unpack(x[k], i);
-                if (d < a.rd) {
-                  const float xc = __fmul_rn(z[i], s_cos[r][j]), ys = __fmul_rn(y[i], s_sin[r][j]);
-                  z[i] = d < half ? __fsub_rn(xc, ys) : __fadd_rn(xc, ys);
-                }
-              }
-              x[k] = make_uint4(pack2(z[0], z[1]), pack2(z[2], z[3]), pack2(z[4], z[5]), pack2(z[6], z[7]));
+            for (int i = 0; i < 4; ++i) {
+              const f2 lo = unpack2(word(x[k], i)), hi = unpack2(word(y[k], i));
+              word(x[k], i) = pack2(add2(mul2(lo, c2[i]), mul2(hi, n2[i])));
+              word(y[k], i) = pack2(add2(mul2(hi, c2[i]), mul2(lo, s2[i])));
             }
           }
-          if (!live) continue;
-          const int h = isq ? u : isk ? u - nqu : u - nqu - P.nkv;
-          uint16_t* dst = isq ? a.qo + t * a.qos + h * 128
-                          : slot >= 0 ? (isk ? P.kp : P.vp) + slot + ((long long)h << P.lps) * 128 : nullptr;
-          if (dst) *reinterpret_cast<uint4*>(dst + d0) = x[k];
+          uint16_t* dst = target(u);
+          if (dst) {
+            *reinterpret_cast<uint4*>(dst + d0) = x[k];
+            *reinterpret_cast<uint4*>(dst + d1) = y[k];
+          }
         }
       }
+    } else {
+      for (int u0 = 0; u0 < units; u0 += HS) {  // a warp's lanes stay together: q_out may be q
+        const int u = u0 + h0, e0 = 8 * (threadIdx.x & 15);
+        const bool live = u < units, turn = u < nqu + P.nkv && e0 < a.rd;
+        const uint16_t* src = source(t, live ? u : 0);
+        uint4 w = *reinterpret_cast<const uint4*>(src + e0);
+        float partner[8];
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const int u = u0 + k * HS + h0;
-        src[k] += u < nqu ? a.qs : u < nqu + P.nkv ? a.ks : a.vs;
+        for (int i = 0; i < 8; ++i) {
+          const int d = e0 + i;
+          partner[i] = turn && d < a.rd ? bf16_bits_to_float(src[d < half ? d + half : d - half]) : 0.f;
+        }
+        __syncwarp();  // every lane has read its head
+        if (turn) {
+          float z[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int d = e0 + i, j = d < half ? d : d - half;
+            const uint32_t pair = word(w, i >> 1);
+            z[i] = (i & 1) ? __uint_as_float(pair & 0xFFFF0000u) : __uint_as_float(pair << 16);
+            if (d < a.rd) {
+              const float xc = __fmul_rn(z[i], s_cos[r][j]), ys = __fmul_rn(partner[i], s_sin[r][j]);
+              z[i] = d < half ? __fsub_rn(xc, ys) : __fadd_rn(xc, ys);
+            }
+          }
+          w = make_uint4(pack2(z[0], z[1]), pack2(z[2], z[3]), pack2(z[4], z[5]), pack2(z[6], z[7]));
+        }
+        uint16_t* dst = live ? target(u) : nullptr;
+        if (dst) *reinterpret_cast<uint4*>(dst + e0) = w;
       }
     }
   }
@@ -201,7 +221,7 @@ __global__ void __launch_bounds__(kApThreads) k_paged_append(const __grid_consta
 
 cudaError_t launch_paged_append(const PagedAppendArgs& a0, cudaStream_t s) {
   PagedAppendArgs a = a0;
-  a.rows = a.p.T >= kApRows * 2 * num_sms() ? kApRows : 1;
+  a.rows = a.p.T >= kApRows * 4 * num_sms() ? kApRows : 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((a.p.T + a.rows - 1) / a.rows);
   cfg.blockDim = dim3(kApThreads);

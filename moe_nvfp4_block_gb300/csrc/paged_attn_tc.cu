@@ -13,9 +13,8 @@
 // same queries again, so that the scores also lie in the tensor memory lanes
 // that the other two of an SM's four warp slots reach: thread (row, half)
 // owns 32 scores of a row, and maximum and sum need one exchange with one
-// other thread.  (64 scores a thread, on two of the four schedulers: 234 us
-// for two sequences of ~100,000 positions and 64 rows, TODO here, 349 by
-// mma.sync.)  For O, rows 64-127 read whatever follows P and end where nobody
+// other thread.  (Two sequences of 65,003 and 131,001 positions, 64 rows, 8 KV
+// heads: 136 us, 5.9 TB/s; by mma.sync 349.)  For O, rows 64-127 read whatever follows P and end where nobody
 // looks.
 //
 // Two groups of four such warps take even and odd chunks, each with its own
@@ -580,67 +579,65 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
         if (lane == 0) mbar_arrive(&T.p_full[g]);
       }
       if (!ok) break;
-      {
-        // ---------------------------------------------------------------- the segment's end
-        // The second half's l joins the first's, and the groups hand theirs
-        // over; then the two groups' first warps add both groups' sums, the
-        // one's 64 dims and the other's.
-        if (seg > 0) ok = wait(&T.epi_done, (uint32_t)(seg - 1) & 1u);
+      // ---------------------------------------------------------------- the segment's end
+      // The second half's l joins the first's, and the groups hand theirs
+      // over; then the two groups' first warps add both groups' sums, the
+      // one's 64 dims and the other's.
+      if (seg > 0) ok = wait(&T.epi_done, (uint32_t)(seg - 1) & 1u);
+      if (!ok) break;
+      if (half == 1) T.l[g][row] = l;
+      if (!(ok = exchange())) break;
+      if (half == 0) {
+        T.l[g][row] += l;
+        T.m[g][row] = m;
+        if (row == 0) T.has[g] = has;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&T.ml_full);
+        const int n0 = (st1 + 1) >> 1, n1 = st1 >> 1;  // the groups' chunks so far
+        ok = wait(&T.ml_full, (uint32_t)seg & 1u);
+        const bool has0 = ok && T.has[0], has1 = ok && T.has[1];
+        if (ok && has0) ok = wait(&T.o_done[0], (uint32_t)(n0 - 1) & 1u);
+        if (ok && has1) ok = wait(&T.o_done[1], (uint32_t)(n1 - 1) & 1u);
         if (!ok) break;
-        if (half == 1) T.l[g][row] = l;
-        if (!(ok = exchange())) break;
-        if (half == 0) {
-          T.l[g][row] += l;
-          T.m[g][row] = m;
-          if (row == 0) T.has[g] = has;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&T.ml_full);
-          const int n0 = (st1 + 1) >> 1, n1 = st1 >> 1;  // the groups' chunks so far
-          ok = wait(&T.ml_full, (uint32_t)seg & 1u);
-          const bool has0 = ok && T.has[0], has1 = ok && T.has[1];
-          if (ok && has0) ok = wait(&T.o_done[0], (uint32_t)(n0 - 1) & 1u);
-          if (ok && has1) ok = wait(&T.o_done[1], (uint32_t)(n1 - 1) & 1u);
-          if (!ok) break;
-          tc_fence_after();
-          const float m0 = has0 ? T.m[0][row] : -INFINITY, m1 = has1 ? T.m[1][row] : -INFINITY, M = fmaxf(m0, m1);
-          const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - M), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
-          const float L = (has0 ? T.l[0][row] : 0.f) * f0 + (has1 ? T.l[1][row] : 0.f) * f1;
-          const bool whole = D.parts == 1;
-          const size_t prow = (size_t)(cta * 2 + D.slot) * rows + row;
-          const float f = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
+        tc_fence_after();
+        const float m0 = has0 ? T.m[0][row] : -INFINITY, m1 = has1 ? T.m[1][row] : -INFINITY, M = fmaxf(m0, m1);
+        const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - M), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
+        const float L = (has0 ? T.l[0][row] : 0.f) * f0 + (has1 ? T.l[1][row] : 0.f) * f1;
+        const bool whole = D.parts == 1;
+        const size_t prow = (size_t)(cta * 2 + D.slot) * rows + row;
+        const float f = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
 #pragma unroll 1
-          for (int c = 64 * g; c < 64 * g + 64; c += 32) {
-            uint32_t o0[32], o1[32];
-            float v[32];
-            if (has0) tc_ld32(tmem + t_lane + kTcO + c, o0);
-            if (has1) tc_ld32(tmem + t_lane + kTcO + 128 + c, o1);
-            tc_wait_ld();
+        for (int c = 64 * g; c < 64 * g + 64; c += 32) {
+          uint32_t o0[32], o1[32];
+          float v[32];
+          if (has0) tc_ld32(tmem + t_lane + kTcO + c, o0);
+          if (has1) tc_ld32(tmem + t_lane + kTcO + 128 + c, o1);
+          tc_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              v[i] = has0 ? __uint_as_float(o0[i]) * f0 : 0.f;
-              if (has1) v[i] += __uint_as_float(o1[i]) * f1;
-            }
-            if (live && whole) {
-              uint4* out = reinterpret_cast<uint4*>(a.o + (D.q0 + r) * a.os + h * 128 + c);
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                out[i] = make_uint4(pa_pack(v[8 * i] * f, v[8 * i + 1] * f), pa_pack(v[8 * i + 2] * f, v[8 * i + 3] * f),
-                                    pa_pack(v[8 * i + 4] * f, v[8 * i + 5] * f), pa_pack(v[8 * i + 6] * f, v[8 * i + 7] * f));
-            } else if (live) {
-              float4* out = reinterpret_cast<float4*>(A.part_o + prow * 128 + c);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) __stcg(out + i, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
-            }
+          for (int i = 0; i < 32; ++i) {
+            v[i] = has0 ? __uint_as_float(o0[i]) * f0 : 0.f;
+            if (has1) v[i] += __uint_as_float(o1[i]) * f1;
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&T.epi_done);
-          if (g == 0) {
-            if (live && whole && a.lse)
-              a.lse[(size_t)(D.q0 + r) * a.nq + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-            if (live && !whole) __stcg(reinterpret_cast<float2*>(A.part_ml + 2 * prow), make_float2(M, L));
-            if (!whole && row == 0) A.rec[cta * 2 + D.slot] = {D.cf, D.parts, D.q0, D.n, D.kvh};
+          if (live && whole) {
+            uint4* out = reinterpret_cast<uint4*>(a.o + (D.q0 + r) * a.os + h * 128 + c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              out[i] = make_uint4(pa_pack(v[8 * i] * f, v[8 * i + 1] * f), pa_pack(v[8 * i + 2] * f, v[8 * i + 3] * f),
+                                  pa_pack(v[8 * i + 4] * f, v[8 * i + 5] * f), pa_pack(v[8 * i + 6] * f, v[8 * i + 7] * f));
+          } else if (live) {
+            float4* out = reinterpret_cast<float4*>(A.part_o + prow * 128 + c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) __stcg(out + i, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
           }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&T.epi_done);
+        if (g == 0) {
+          if (live && whole && a.lse)
+            a.lse[(size_t)(D.q0 + r) * a.nq + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+          if (live && !whole) __stcg(reinterpret_cast<float2*>(A.part_ml + 2 * prow), make_float2(M, L));
+          if (!whole && row == 0) A.rec[cta * 2 + D.slot] = {D.cf, D.parts, D.q0, D.n, D.kvh};
         }
       }
       done(seg);
