@@ -66,13 +66,16 @@ struct TcTable {
   uint64_t o_done[2];   // the product with P of group g is done
   uint64_t q_full, q_empty;  // the segment's Q is there; its last product with it is done
   uint64_t ml_full;     // the segment's m and l are there
-  uint64_t epi_done;    // the segment's outputs are out of tensor memory
+  uint64_t epi_done;    // the segment's outputs are out of tensor memory (a group's first P of the next waits)
   uint64_t fin[2];
   uint32_t tmem;
   int pv[2];            // slices to multiply (bits 0-3); bit 4: O holds sums already
-  float top[2][2][64];  // [group][half][row] maximum of a chunk's scores
-  int odd[2][4];        // [group][warp] slices where it saw infinite or NaN values
-  float m[2][64], l[2][64];
+  // [group's chunk mod 2][group][half][row] maximum of a chunk's scores.  (A
+  // warp may be a chunk ahead of the one that reads what it wrote, not two.)
+  // At a segment's end the place of the group's next chunk takes its m and l
+  // ([0][row], [1][row]) until the outputs are out (epi_done).
+  float top[2][2][2][64];
+  int odd[2][2][4];     // [chunk mod 2][group][warp] slices where it saw infinite or NaN values
   int has[2];           // the group has sums
 };
 
@@ -303,8 +306,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
           ok = wait(&T.p_full[g], (uint32_t)(st >> 1) & 1u);
           if (!ok) break;
           const int pv = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&T.pv[g]), 0);
-          if ((pv & 15) && !(pv & 16) && seg > 0) ok = wait(&T.epi_done, (uint32_t)(seg - 1) & 1u);
-          if (!ok) break;
           tc_fence_after();
           const uint64_t p = p0 + (unsigned)(g * (kTcP >> 4)), v = v0 + (unsigned)(sl * (kPaStageBytes >> 4));
           const uint32_t d = tmem + kTcO + 128 * g;
@@ -403,7 +404,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
       const int st0 = D.st0, st1 = st0 + D.count;
       if (st0 == st1) break;
       float m = -INFINITY, l = 0.f, slope = 0.f;
-      bool has = false;
+      bool has = false, clean = seg == 0;  // clean: the last segment's outputs are out
+      auto cleaned = [&]() {
+        if (!clean) ok = wait(&T.epi_done, (uint32_t)(seg - 1) & 1u);
+        clean = true;
+        return ok;
+      };
       const bool live = row < D.n * a.group;
       const int r = live ? row / a.group : 0, h = D.kvh * a.group + (live ? row - r * a.group : 0);
       const int rp = D.len + r;  // the row's position
@@ -455,7 +461,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int c = 0; c < 32; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
-        T.top[g][half][row] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (!cleaned()) break;
+        float(&s_top)[2][64] = T.top[own & 1][g];
+        int(&s_odd)[4] = T.odd[own & 1][g];
+        s_top[half][row] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         const uint32_t v0 = smem_addr(ring + (size_t)sl * kPaStageBytes + kPaHalf);
         if (any & ~clear) {
           // slices with hidden positions: infinite or NaN values among them?
@@ -479,10 +488,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
             }
             odd |= __any_sync(0xffffffffu, bad) << ks;
           }
-          if (lane == 0) T.odd[g][warp & 3] = odd;
+          if (lane == 0) s_odd[warp & 3] = odd;
         }
         if (!(ok = exchange())) break;
-        const float top = fmaxf(T.top[g][0][row], T.top[g][1][row]);
+        const float top = fmaxf(s_top[0][row], s_top[1][row]);
         float scale = 1.f;
         if (top > m && (m == -INFINITY || top - m > kTcLazy)) {
           if (m != -INFINITY) scale = ex2(m - top);  // else the row's sums are zeros
@@ -530,15 +539,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
         }
         int pv = any;
         if (any & ~clear) {
-          const int odd = T.odd[g][0] | T.odd[g][1] | T.odd[g][2] | T.odd[g][3];
+          const int odd = s_odd[0] | s_odd[1] | s_odd[2] | s_odd[3];
           if (odd) {
             pv &= ~odd;
             // (the same for all four warps) the other half of the rows' P
             if (!(ok = exchange())) break;
-            // these tensor memory lanes may still be read for the segment before
-            if (!has && seg > 0) ok = wait(&T.epi_done, (uint32_t)(seg - 1) & 1u);
-            if (!ok) break;
-            tc_fence_after();
 #pragma unroll 1
             for (int c = 0; half == 0 && c < 128; c += 32) {
               uint32_t o[32];
@@ -583,26 +588,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
       // The second half's l joins the first's, and the groups hand theirs
       // over; then the two groups' first warps add both groups' sums, the
       // one's 64 dims and the other's.
-      if (seg > 0) ok = wait(&T.epi_done, (uint32_t)(seg - 1) & 1u);
-      if (!ok) break;
-      if (half == 1) T.l[g][row] = l;
+      const int n0 = (st1 + 1) >> 1, n1 = st1 >> 1;  // the groups' chunks so far
+      float(&s_ml)[2][64] = T.top[(g ? n1 : n0) & 1][g];
+      if (!cleaned()) break;
+      if (half == 1) s_ml[1][row] = l;
       if (!(ok = exchange())) break;
       if (half == 0) {
-        T.l[g][row] += l;
-        T.m[g][row] = m;
+        s_ml[0][row] = m;
+        s_ml[1][row] += l;
         if (row == 0) T.has[g] = has;
         __syncwarp();
         if (lane == 0) mbar_arrive(&T.ml_full);
-        const int n0 = (st1 + 1) >> 1, n1 = st1 >> 1;  // the groups' chunks so far
         ok = wait(&T.ml_full, (uint32_t)seg & 1u);
         const bool has0 = ok && T.has[0], has1 = ok && T.has[1];
         if (ok && has0) ok = wait(&T.o_done[0], (uint32_t)(n0 - 1) & 1u);
         if (ok && has1) ok = wait(&T.o_done[1], (uint32_t)(n1 - 1) & 1u);
         if (!ok) break;
         tc_fence_after();
-        const float m0 = has0 ? T.m[0][row] : -INFINITY, m1 = has1 ? T.m[1][row] : -INFINITY, M = fmaxf(m0, m1);
+        const float(&ml0)[2][64] = T.top[n0 & 1][0], (&ml1)[2][64] = T.top[n1 & 1][1];
+        const float m0 = has0 ? ml0[0][row] : -INFINITY, m1 = has1 ? ml1[0][row] : -INFINITY, M = fmaxf(m0, m1);
         const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - M), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
-        const float L = (has0 ? T.l[0][row] : 0.f) * f0 + (has1 ? T.l[1][row] : 0.f) * f1;
+        const float L = (has0 ? ml0[1][row] : 0.f) * f0 + (has1 ? ml1[1][row] : 0.f) * f1;
         const bool whole = D.parts == 1;
         const size_t prow = (size_t)(cta * 2 + D.slot) * rows + row;
         const float f = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
