@@ -79,15 +79,17 @@ __global__ void __launch_bounds__(kLlWarps * 32, 1) k_lmhead_logits(const __grid
   const int nst = g0 < ngrp ? ((ngrp - 1 - g0) / step + 1) * nblk : 0;
   volatile int* abort = &T.abort;
   // stage s: column block s % nblk of the group g0 + (s / nblk) step
-  auto issue = [&](int s, uint64_t pol) {
+  const uint64_t pol = policy_evict_first();
+  auto issue = [&](int s) {  // by the whole warp, a row a lane
     const int grp = g0 + s / nblk * step, c0 = s % nblk * kLlCols;
     const uint32_t bytes = (uint32_t)min(kLlCols, H - c0) * 2u;
     const int nr = min(kLlRows, V - grp * kLlRows);
     uint64_t* bar = &T.full[warp][s % kLlSlots];
-    unsigned char* dst = ring + (size_t)(s % kLlSlots) * kLlSlotBytes;
-    mbar_arrive_expect_tx(bar, bytes * nr);
-    for (int q = 0; q < nr; ++q)
-      bulk_load(dst + q * (kLlCols * 2), a.W + (size_t)(grp * kLlRows + q) * H + c0, bytes, bar, pol);
+    if (lane == 0) mbar_arrive_expect_tx(bar, bytes * nr);
+    __syncwarp();
+    if (lane < nr)
+      bulk_load(ring + (size_t)(s % kLlSlots) * kLlSlotBytes + lane * (kLlCols * 2),
+                a.W + (size_t)(grp * kLlRows + lane) * H + c0, bytes, bar, pol);
   };
   if (lane == 0) {
     for (int i = 0; i < kLlSlots; ++i) mbar_init(&T.full[warp][i], 1);
@@ -95,11 +97,7 @@ __global__ void __launch_bounds__(kLlWarps * 32, 1) k_lmhead_logits(const __grid
     fence_mbar_init();
   }
   __syncthreads();
-  uint64_t pol = 0;
-  if (lane == 0) {
-    pol = policy_evict_first();
-    for (int s = 0; s < min(nst, kLlSlots); ++s) issue(s, pol);
-  }
+  for (int s = 0; s < min(nst, kLlSlots); ++s) issue(s);
   pdl_launch_dependents();
   // x in planes [row][256 columns][first or second half of a lane's eight][lane][4]:
   // a warp's 8-byte reads are consecutive (all banks)
@@ -159,7 +157,7 @@ __global__ void __launch_bounds__(kLlWarps * 32, 1) k_lmhead_logits(const __grid
       }
     }
     __syncwarp();
-    if (lane == 0 && s + kLlSlots < nst) issue(s + kLlSlots, pol);
+    if (s + kLlSlots < nst) issue(s + kLlSlots);
     if (blk != nblk - 1) continue;
     // sums b = q + 4 r of rows r = 8 h .. 8 h + 7, one a lane
     const int v0 = (g0 + s / nblk * step) * kLlRows;

@@ -32,18 +32,25 @@ namespace {
 
 __device__ __forceinline__ bool lg_better(float a, int i, float b, int j) { return a > b || (a == b && i < j); }
 
-// f[i] += p[i] for the N floats at p = q + MIS floats, q on a 16-byte line.
+// What a line of N tokens is worked with: its logits, the bias's 16-byte lines
+// that hold its N values, the one or two words that hold its mask.
+template <int N>
+struct LgLine {
+  uint4 x;
+  float4 b[N / 4 + 1];
+  uint32_t lo, hi;
+};
+
+// f[i] += the line's i-th bias, the first MIS floats behind the start of b.
 template <int N, int MIS>
-__device__ __forceinline__ void lg_add(const float* p, float (&f)[N]) {
-  const float4* q = reinterpret_cast<const float4*>(p - MIS);
+__device__ __forceinline__ void lg_add(const float4 (&b)[N / 4 + 1], float (&f)[N]) {
   float w[N + 4];
 #pragma unroll
-  for (int i = 0; i < (MIS ? N / 4 + 1 : N / 4); ++i) {
-    const float4 v = __ldg(q + i);
-    w[4 * i] = v.x;
-    w[4 * i + 1] = v.y;
-    w[4 * i + 2] = v.z;
-    w[4 * i + 3] = v.w;
+  for (int i = 0; i < N / 4 + 1; ++i) {
+    w[4 * i] = b[i].x;
+    w[4 * i + 1] = b[i].y;
+    w[4 * i + 2] = b[i].z;
+    w[4 * i + 3] = b[i].w;
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) f[i] = __fadd_rn(f[i], w[i + MIS]);
@@ -189,25 +196,37 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logits(const __grid
       __syncthreads();
     }
     const int end = min(32 * w_hi, e_hi);
-    auto line_at = [&](int e) {
-      return e >= e_lo && e + N <= end ? *reinterpret_cast<const uint4*>(xt + e) : make_uint4(0u, 0u, 0u, 0u);
+    // everything that a line needs from memory, asked for at once
+    auto ask = [&](int e, LgLine<N>& q) {
+      if (e < e_lo || e + N > end) return;
+      const int v = e + j0 - phase;
+      q.x = *reinterpret_cast<const uint4*>(xt + e);
+      if (bias && v >= 4 && v + N + 4 <= V) {  // whole lines, up to 3 floats more on each side
+        const float4* p = reinterpret_cast<const float4*>(bias + e - bias_mis);
+#pragma unroll
+        for (int i = 0; i < N / 4 + 1; ++i) q.b[i] = __ldg(p + i);
+      }
+      if (allow) {
+        q.lo = __ldg(allow + (v >> 5));
+        q.hi = __ldg(allow + ((v + N - 1) >> 5));
+      }
     };
     for (int e1 = 32 * w_lo + tid * N; e1 < end; e1 += kLgDeep * THREADS * N) {
-      uint4 lines[kLgDeep];
+      LgLine<N> lines[kLgDeep];
 #pragma unroll
-      for (int u = 0; u < kLgDeep; ++u) lines[u] = line_at(e1 + u * THREADS * N);
+      for (int u = 0; u < kLgDeep; ++u) ask(e1 + u * THREADS * N, lines[u]);
 #pragma unroll
       for (int u = 0; u < kLgDeep; ++u) {
         const int e0 = e1 + u * THREADS * N;
         if (e0 >= end) break;
-        const uint4 line = lines[u];
+        const LgLine<N>& q = lines[u];
         const int v = e0 + j0 - phase;
         unsigned hit = 0;
         if (n > 0) hit = (s_bits[e0 >> 5] >> (e0 & 31)) & ((1u << N) - 1u);
         auto listed = [&]() { return s_pre[e0 >> 5] - p0 + __popc(s_bits[e0 >> 5] & ((1u << (e0 & 31)) - 1u)); };
         if (e0 >= e_lo && e0 + N <= e_hi) {
           T e[N];
-          memcpy(e, &line, 16);
+          memcpy(e, &q.x, 16);
           float f[N];
 #pragma unroll
           for (int i = 0; i < N; ++i) f[i] = load(e[i]);
@@ -218,12 +237,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logits(const __grid
               if (hit >> i & 1) f[i] = __int_as_float(s_cnt[at++]);
           }
           if (bias) {
-            if (v >= 4 && v + N + 4 <= V) {  // whole lines, up to 3 floats more on each side
+            if (v >= 4 && v + N + 4 <= V) {
               switch (bias_mis) {
-                case 0: lg_add<N, 0>(bias + e0, f); break;
-                case 1: lg_add<N, 1>(bias + e0, f); break;
-                case 2: lg_add<N, 2>(bias + e0, f); break;
-                default: lg_add<N, 3>(bias + e0, f); break;
+                case 0: lg_add<N, 0>(q.b, f); break;
+                case 1: lg_add<N, 1>(q.b, f); break;
+                case 2: lg_add<N, 2>(q.b, f); break;
+                default: lg_add<N, 3>(q.b, f); break;
               }
             } else {
 #pragma unroll
@@ -231,8 +250,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logits(const __grid
             }
           }
           if (allow) {
-            const uint32_t lo = __ldg(allow + (v >> 5)), hi = __ldg(allow + ((v + N - 1) >> 5));
-            const uint32_t bits = __funnelshift_r(lo, hi, v & 31);
+            const uint32_t bits = __funnelshift_r(q.lo, q.hi, v & 31);
 #pragma unroll
             for (int i = 0; i < N; ++i)
               if (!(bits >> i & 1u)) f[i] = -INFINITY;
