@@ -401,7 +401,7 @@ struct LogitArgs {
   float* part_v;              // [R][ntile] each tile's best
   int* part_i;
 };
-constexpr int kLogitTile = 65536;  // most tokens of a CTA
+constexpr int kLogitTile = 131072;  // most tokens of a CTA
 cudaError_t launch_logits(const LogitArgs& a, cudaStream_t s);
 
 // capi.cu: the limit of device waits; the angles and temperature of a moe_attn_pos

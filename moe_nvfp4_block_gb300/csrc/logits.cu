@@ -5,24 +5,32 @@
 // turned into a short list of the tile's repeated tokens: a bit map of the
 // tile, the number of bits before each of its words, and, by a second look at
 // the history, the tokens' counts at their places in the list.  The penalties
-// (a division among them) are then taken once per listed token, and the walk
-// over all logits only picks them up: penalty, bias, mask, store, running
-// maximum.  More than kLgList listed tokens are worked on a stretch of the
-// tile at a time.  The row's last CTA (a ticket) takes the best of the tiles.
+// (a division among them) are taken once per listed token.  The walk over all
+// logits (bias, mask, store, running maximum) holds listed tokens at -inf, and
+// the list's own pass behind it stores and compares them, in the list's rising
+// order, so that a warp's 32 lie near one another.  More than kLgList listed
+// tokens are worked on a stretch of the tile at a time.  The row's last CTA (a
+// ticket) takes the best of the tiles.
 //
-// What bounds it: the logits read and written once, and how much of a CTA's
-// life its loads fill, so tiles are as long as leaves the SMs evenly filled
-// (a table of counts per token instead of the bit map holds 8192 tokens where
-// this one holds 65,536: 78 us against 67 for 256 rows of 128,003 tokens
-// with histories of 4000, whose every tile then looks through the history
-// again).  So that the arithmetic stays below that, a thread's 16-byte line
-// of 4 or 8 tokens is one step: one look at the bit map, one shifted word of
-// the mask, whole 16-byte loads of the bias, one maximum, and the index is
-// searched only in a line that beats it.
+// What bounds it: the logits read and written once, and above that the
+// instructions of the walk and the looks at the history.  256 rows of 128,003
+// bf16 tokens (131 MB in all, whose plain copy takes 45 us) take 25 us without
+// rules, 39 with biases and masks, 59 with histories of 4000 as well.  So:
+//  * tiles are as long as leaves the SMs evenly filled, since every tile looks
+//    through its row's whole history: 65 us where tiles of 65,536 took 70;
+//  * lines come by cp.async, kLgRing ahead a thread, asked for before the look
+//    at the history (25 us without rules, 37 with plain loads two ahead);
+//  * a thread's 16-byte line of 4 or 8 tokens is one step: one shifted word of
+//    the bit map and one of the mask, whole 16-byte loads of the bias, one
+//    maximum, and the index is searched only in a line that beats the warp's
+//    best (listed tokens picked up inside the walk: 65 us against 59);
+//  * lines over an end of the row take a step of their own.
 //
 // Rows start anywhere (an odd vocabulary): a row's elements are grouped by
 // the 16-byte lines of its input, element j = v + phase with phase the row's
 // offset from a line; whole lines inside the row take one 16-byte load.
+#include <type_traits>
+
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -32,16 +40,7 @@ namespace {
 
 __device__ __forceinline__ bool lg_better(float a, int i, float b, int j) { return a > b || (a == b && i < j); }
 
-// What a line of N tokens is worked with: its logits, the bias's 16-byte lines
-// that hold its N values, the one or two words that hold its mask.
-template <int N>
-struct LgLine {
-  uint4 x;
-  float4 b[N / 4 + 1];
-  uint32_t lo, hi;
-};
-
-// f[i] += the line's i-th bias, the first MIS floats behind the start of b.
+// f[i] += the i-th of the N biases that start MIS floats into b.
 template <int N, int MIS>
 __device__ __forceinline__ void lg_add(const float4 (&b)[N / 4 + 1], float (&f)[N]) {
   float w[N + 4];
@@ -59,12 +58,13 @@ __device__ __forceinline__ void lg_add(const float4 (&b)[N / 4 + 1], float (&f)[
 }  // namespace
 
 constexpr int kLgList = 4096;
-constexpr int kLgDeep = 2;  // lines in flight a thread
+constexpr int kLgRing = 4;  // lines a thread has asked for ahead of the one it works on
 
 template <typename T, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logits(const __grid_constant__ LogitArgs a) {
   constexpr int N = 16 / sizeof(T);  // elements of a line
-  extern __shared__ __align__(16) unsigned s_bits[];  // [tile / 32] bit map
+  extern __shared__ __align__(16) uint4 s_ring[];  // [kLgRing][THREADS] lines of x
+  unsigned* s_bits = reinterpret_cast<unsigned*>(s_ring + kLgRing * THREADS);  // [tile / 32] bit map
   __shared__ float s_bv[THREADS / 32];
   __shared__ int s_bi[THREADS / 32];
   const moe_logit_rules& R = a.rules;
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logits(const __grid
   const int nw = a.tile / 32;
   int* s_pre = reinterpret_cast<int*>(s_bits + nw);               // [nw] bits before the word
   int* s_cnt = s_pre + nw;                                        // [kLgList] counts, then values
-  uint16_t* s_tok = reinterpret_cast<uint16_t*>(s_cnt + kLgList); // [kLgList] elements of the tile
+  int* s_tok = s_cnt + kLgList;                                   // [kLgList] elements of the tile
   pdl_wait();
   pdl_launch_dependents();
   const T* x = static_cast<const T*>(a.x) + r * a.xs;
@@ -83,11 +83,15 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logits(const __grid
   const int j0 = blockIdx.x * a.tile;
   const int e_lo = max(0, phase - j0), e_hi = min(a.tile, V + phase - j0);  // the row's elements
   const T* xt = x + (j0 - phase);
-  // the tile's lines come to L2 while the history is looked at
-  if (R.tokens && tid == 0 && e_lo < e_hi) {
-    const int p0 = (e_lo + N - 1) / N * N, p1 = e_hi / N * N;
-    if (p0 < p1) l2_prefetch_span(xt + p0, (uint64_t)(p1 - p0) * sizeof(T));
-  }
+  // line k of this thread is at element (k THREADS + tid) N; the first ones are
+  // on their way while the history is looked at
+  auto fetch = [&](int k) {
+    const int e = (k * THREADS + tid) * N;
+    if (e >= e_lo && e + N <= e_hi) cp_async_16(&s_ring[k % kLgRing * THREADS + tid], xt + e);
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int k = 0; k < kLgRing; ++k) fetch(k);
   auto load = [](T e) {
     if constexpr (sizeof(T) == 4) return (float)e;
     else return bf16_bits_to_float(e);
@@ -97,6 +101,15 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logits(const __grid
     else return (T)float_to_bf16_bits(f);
   };
 
+  // the row's parameters, all asked for before the first wait
+  const int brow = R.bias ? R.bias_row[r] : -1, arow = R.allow ? R.allow_row[r] : -1;
+  const float* bias = brow >= 0 && brow < R.n_bias ? R.bias + (size_t)brow * V + (j0 - phase) : nullptr;
+  const uint32_t* allow = arow >= 0 && arow < R.n_allow ? R.allow + (size_t)arow * ((V + 31) / 32) : nullptr;
+  // where the tile's lines start in the bias: the same for all of them
+  const int bias_mis = (int)((reinterpret_cast<uintptr_t>(bias) >> 2) & 3);
+  const float rep = R.tokens && R.repetition ? R.repetition[r] : 1.f;
+  const float pres = R.tokens && R.presence ? R.presence[r] : 0.f;
+  const float freq = R.tokens && R.frequency ? R.frequency[r] : 0.f;
   int h0 = 0, h1 = 0, n = 0;  // the history; listed tokens of the tile
   // f(e) for every token of the history that is element e of the tile
   auto history = [&](auto f) {
@@ -150,30 +163,110 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logits(const __grid
       __syncthreads();
     }
   }
-  const int brow = R.bias ? R.bias_row[r] : -1, arow = R.allow ? R.allow_row[r] : -1;
-  const float* bias = brow >= 0 && brow < R.n_bias ? R.bias + (size_t)brow * V + (j0 - phase) : nullptr;
-  const uint32_t* allow = arow >= 0 && arow < R.n_allow ? R.allow + (size_t)arow * ((V + 31) / 32) : nullptr;
-  if (((R.bias && brow >= R.n_bias) || (R.allow && arow >= R.n_allow)) && tid == 0)
-    atomicCAS(a.err, 0, (int)MOE_ERR_INVALID_ARG);
-  // where the tile's lines start in the bias: the same for all of them
-  const int bias_mis = (int)((reinterpret_cast<uintptr_t>(bias) >> 2) & 3);
-
   float bv = -INFINITY;
-  int bi = -1;
+  int bi = -1, k = 0;
+  float wmax = -INFINITY;  // of the warp's lanes' bv
+  auto warp_max = [](float x) {
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+    return x;
+  };
+  // The warp's lines of step k: bias, mask, store, maximum.  A listed token is
+  // stored and compared behind the walk, and is -inf here.  EDGE: lines or
+  // their bias may reach over an end of the row.
+  auto step = [&](int k, auto edge) {
+    constexpr bool EDGE = decltype(edge)::value;
+    const int e0 = (k * THREADS + tid) * N, v = e0 + j0 - phase;
+    const bool whole = !EDGE || (e0 >= e_lo && e0 + N <= e_hi);
+    unsigned in = (1u << N) - 1u;  // which tokens of the line are the row's
+    if (EDGE && !whole) {
+      in = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) in |= e0 + i >= e_lo && e0 + i < e_hi ? 1u << i : 0u;
+    }
+    // what comes from memory besides the ring, asked for before any is used
+    float4 b[N / 4 + 1];
+    uint32_t bits = in;
+    const bool wide = bias && (!EDGE || (v >= 4 && v + N + 4 <= V));  // whole lines of the bias: 3 floats more on a side
+    if (wide) {
+      const float4* p = reinterpret_cast<const float4*>(bias + e0 - bias_mis);
+#pragma unroll
+      for (int i = 0; i < N / 4 + 1; ++i) b[i] = __ldg(p + i);
+    }
+    if (allow && in) {
+      const int v0 = EDGE ? max(v, 0) : v, v1 = EDGE ? min(v + N, V) - 1 : v + N - 1;
+      bits = __funnelshift_r(__ldg(allow + (v0 >> 5)), __ldg(allow + (v1 >> 5)), v0 & 31) << (v0 - v) & in;
+    }
+    if (n > 0 && in) bits &= ~(s_bits[e0 >> 5] >> (e0 & 31));
+    cp_async_wait<kLgRing - 1>();
+    const uint4 line = s_ring[k % kLgRing * THREADS + tid];
+    fetch(k + kLgRing);
+    T e[N];
+    memcpy(e, &line, 16);
+    if (EDGE && !whole)
+#pragma unroll
+      for (int i = 0; i < N; ++i) e[i] = in >> i & 1u ? xt[e0 + i] : (T)0;
+    float f[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = load(e[i]);
+    if (wide) {
+      switch (bias_mis) {
+        case 0: lg_add<N, 0>(b, f); break;
+        case 1: lg_add<N, 1>(b, f); break;
+        case 2: lg_add<N, 2>(b, f); break;
+        default: lg_add<N, 3>(b, f); break;
+      }
+    } else if (EDGE && bias) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (in >> i & 1u) f[i] = __fadd_rn(f[i], bias[e0 + i]);
+    }
+    if (bits != (1u << N) - 1u) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (!(bits >> i & 1u)) f[i] = -INFINITY;
+    }
+    float top = f[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) top = fmaxf(top, f[i]);
+    if (__any_sync(0xffffffffu, top > wmax)) {
+      if (top > wmax) {
+        bv = top;
+#pragma unroll
+        for (int i = N - 1; i >= 0; --i)
+          if (f[i] == top) bi = v + i;
+      }
+      wmax = warp_max(bv);
+    }
+    if (out) {
+      if (whole && same) {
+        uint4 w;
+        if constexpr (N == 4)
+          w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+        else
+          w = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+        *reinterpret_cast<uint4*>(out + v) = w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (!EDGE || (in >> i & 1u)) out[v + i] = store(f[i]);
+      }
+    }
+  };
   // stretches [w_lo, w_hi) of the bit map's words with at most kLgList listed tokens
   for (int w_lo = 0, w_hi; w_lo < nw; w_lo = w_hi) {
     w_hi = nw;
     const int p0 = n > 0 ? s_pre[w_lo] : 0;
     if (n > 0) {
       int m = n - p0;
-      if (m > kLgList) {  // the last word that still fits
-        int lo = w_lo + 1, hi = nw - 1;
+      if (m > kLgList) {  // as many of a warp's lines (N words) as fit
+        int lo = w_lo / N + 1, hi = nw / N - 1;
         while (lo < hi) {
           const int mid = (lo + hi + 1) >> 1;
-          if (s_pre[mid] - p0 <= kLgList) lo = mid;
+          if (s_pre[mid * N] - p0 <= kLgList) lo = mid;
           else hi = mid - 1;
         }
-        w_hi = lo;
+        w_hi = lo * N;
         m = s_pre[w_hi] - p0;
       }
       for (int i = tid; i < m; i += THREADS) s_cnt[i] = 0;
@@ -183,117 +276,52 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logits(const __grid
         if (w < w_lo || w >= w_hi) return;
         const int i = s_pre[w] - p0 + __popc(s_bits[w] & ((1u << (e & 31)) - 1u));
         atomicAdd(&s_cnt[i], 1);
-        s_tok[i] = (uint16_t)e;
+        s_tok[i] = e;
       });
       __syncthreads();
-      const float rep = R.repetition ? R.repetition[r] : 1.f;
-      const float pres = R.presence ? R.presence[r] : 0.f, freq = R.frequency ? R.frequency[r] : 0.f;
-      for (int i = tid; i < m; i += THREADS) {
-        float f = load(xt[s_tok[i]]);
-        f = f > 0.f ? __fdiv_rn(f, rep) : __fmul_rn(f, rep);
-        s_cnt[i] = __float_as_int(__fsub_rn(f, __fadd_rn(pres, __fmul_rn((float)s_cnt[i], freq))));
+      for (int i0 = tid; i0 < m; i0 += 4 * THREADS) {
+        T xl[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) xl[u] = i0 + u * THREADS < m ? xt[s_tok[i0 + u * THREADS]] : (T)0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = i0 + u * THREADS;
+          if (i >= m) break;
+          float f = load(xl[u]);
+          f = f > 0.f ? __fdiv_rn(f, rep) : __fmul_rn(f, rep);
+          s_cnt[i] = __float_as_int(__fsub_rn(f, __fadd_rn(pres, __fmul_rn((float)s_cnt[i], freq))));
+        }
       }
       __syncthreads();
     }
+    // this warp's lines of the stretch, 32 at a time
     const int end = min(32 * w_hi, e_hi);
-    // everything that a line needs from memory, asked for at once
-    auto ask = [&](int e, LgLine<N>& q) {
-      if (e < e_lo || e + N > end) return;
-      const int v = e + j0 - phase;
-      q.x = *reinterpret_cast<const uint4*>(xt + e);
-      if (bias && v >= 4 && v + N + 4 <= V) {  // whole lines, up to 3 floats more on each side
-        const float4* p = reinterpret_cast<const float4*>(bias + e - bias_mis);
-#pragma unroll
-        for (int i = 0; i < N / 4 + 1; ++i) q.b[i] = __ldg(p + i);
-      }
-      if (allow) {
-        q.lo = __ldg(allow + (v >> 5));
-        q.hi = __ldg(allow + ((v + N - 1) >> 5));
-      }
-    };
-    for (int e1 = 32 * w_lo + tid * N; e1 < end; e1 += kLgDeep * THREADS * N) {
-      LgLine<N> lines[kLgDeep];
-#pragma unroll
-      for (int u = 0; u < kLgDeep; ++u) ask(e1 + u * THREADS * N, lines[u]);
-#pragma unroll
-      for (int u = 0; u < kLgDeep; ++u) {
-        const int e0 = e1 + u * THREADS * N;
-        if (e0 >= end) break;
-        const LgLine<N>& q = lines[u];
-        const int v = e0 + j0 - phase;
-        unsigned hit = 0;
-        if (n > 0) hit = (s_bits[e0 >> 5] >> (e0 & 31)) & ((1u << N) - 1u);
-        auto listed = [&]() { return s_pre[e0 >> 5] - p0 + __popc(s_bits[e0 >> 5] & ((1u << (e0 & 31)) - 1u)); };
-        if (e0 >= e_lo && e0 + N <= e_hi) {
-          T e[N];
-          memcpy(e, &q.x, 16);
-          float f[N];
-#pragma unroll
-          for (int i = 0; i < N; ++i) f[i] = load(e[i]);
-          if (hit) {
-            int at = listed();
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-              if (hit >> i & 1) f[i] = __int_as_float(s_cnt[at++]);
-          }
-          if (bias) {
-            if (v >= 4 && v + N + 4 <= V) {
-              switch (bias_mis) {
-                case 0: lg_add<N, 0>(q.b, f); break;
-                case 1: lg_add<N, 1>(q.b, f); break;
-                case 2: lg_add<N, 2>(q.b, f); break;
-                default: lg_add<N, 3>(q.b, f); break;
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < N; ++i) f[i] = __fadd_rn(f[i], bias[e0 + i]);
-            }
-          }
-          if (allow) {
-            const uint32_t bits = __funnelshift_r(q.lo, q.hi, v & 31);
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-              if (!(bits >> i & 1u)) f[i] = -INFINITY;
-          }
-          float top = f[0];
-#pragma unroll
-          for (int i = 1; i < N; ++i) top = fmaxf(top, f[i]);
-          if (top > bv) {
-            bv = top;
-#pragma unroll
-            for (int i = N - 1; i >= 0; --i)
-              if (f[i] == top) bi = v + i;
-          }
-          if (out) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) e[i] = store(f[i]);
-            if (same) {
-              uint4 w;
-              memcpy(&w, e, 16);
-              *reinterpret_cast<uint4*>(out + v) = w;
-            } else {
-#pragma unroll
-              for (int i = 0; i < N; ++i) out[v + i] = e[i];
-            }
-          }
-        } else {  // a row's first or last line, in part
-          int at = hit ? listed() : 0;
-          for (int i = max(0, e_lo - e0); i < N && e0 + i < e_hi; ++i) {
-            float f = load(xt[e0 + i]);
-            if (hit >> i & 1) f = __int_as_float(s_cnt[at++]);
-            if (bias) f = __fadd_rn(f, bias[e0 + i]);
-            if (allow && !((allow[(v + i) >> 5] >> ((v + i) & 31)) & 1u)) f = -INFINITY;
-            if (f > bv) {
-              bv = f;
-              bi = v + i;
-            }
-            if (out) out[v + i] = store(f);
-          }
+    for (int ew; (ew = (k * THREADS + 32 * warp) * N) < end; ++k) {
+      const int vw = ew + j0 - phase;
+      if (vw >= 4 && vw + 32 * N + 4 <= V && ew + 32 * N <= e_hi) step(k, std::false_type{});
+      else step(k, std::true_type{});
+    }
+    __syncthreads();
+    // the stretch's listed tokens
+    if (n > 0) {
+      const int m = (w_hi < nw ? s_pre[w_hi] : n) - p0;
+      for (int i = tid; i < m; i += THREADS) {
+        const int e = s_tok[i], v = e + j0 - phase;
+        float f = __int_as_float(s_cnt[i]);
+        if (bias) f = __fadd_rn(f, bias[e]);
+        if (allow && !(__ldg(allow + (v >> 5)) >> (v & 31) & 1u)) f = -INFINITY;
+        if (out) out[v] = store(f);
+        if (lg_better(f, v, bv, bi)) {
+          bv = f;
+          bi = v;
         }
       }
+      wmax = warp_max(bv);
     }
     __syncthreads();  // the list is free
   }
+  if (((R.bias && brow >= R.n_bias) || (R.allow && arow >= R.n_allow)) && tid == 0)
+    atomicCAS(a.err, 0, (int)MOE_ERR_INVALID_ARG);
   if (!a.tok && !a.best) return;
   auto warp_best = [&]() {
 #pragma unroll
@@ -317,6 +345,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logits(const __grid
   bi = lane < THREADS / 32 ? s_bi[lane] : -1;
   warp_best();
   unsigned last = 0;
+  if (a.ntile == 1) {
+    if (lane == 0) {
+      if (a.tok) a.tok[r] = bi;
+      if (a.best) a.best[r] = bv;
+    }
+    return;
+  }
   if (lane == 0) {
     a.part_v[(size_t)r * a.ntile + blockIdx.x] = bv;
     a.part_i[(size_t)r * a.ntile + blockIdx.x] = bi;
@@ -365,11 +400,12 @@ cudaError_t launch_logits(const LogitArgs& a0, cudaStream_t s) {
   a.tile = logit_tile(a.R, a.V);
   a.ntile = (a.V + 7 + a.tile - 1) / a.tile;  // the phase shifts a row by up to 7 elements
   const bool wide = a.tile > 4096;
-  const auto bytes = [](int tile) { return tile / 4 + 6 * kLgList; };
+  const auto ring = [](int threads) { return 16 * kLgRing * threads; };
+  const auto list = [](int tile) { return tile / 4 + 8 * kLgList; };
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.ntile, a.R);
   cfg.blockDim = dim3(wide ? 512 : 256);
-  cfg.dynamicSmemBytes = a.rules.tokens ? bytes(a.tile) : 0;
+  cfg.dynamicSmemBytes = ring(wide ? 512 : 256) + (a.rules.tokens ? list(a.tile) : 0);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -377,7 +413,7 @@ cudaError_t launch_logits(const LogitArgs& a0, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   auto run = [&](auto kern, cudaError_t e) { return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, kern, a) : e; };
-  const int most = bytes(kLogitTile);
+  const int most = ring(512) + list(kLogitTile);
   if (wide)
     return a.bf16 ? run(k_logits<uint16_t, 512>, prepare_kernel<k_logits<uint16_t, 512>>(most))
                   : run(k_logits<float, 512>, prepare_kernel<k_logits<float, 512>>(most));
