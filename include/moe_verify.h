@@ -526,7 +526,8 @@ typedef struct {
  * A row that sees no position (or only scores of -inf) gives o = 0.  What
  * hidden positions hold (NaN and infinities too) changes nothing.
  *   q  bf16 [n_rows][nq * 128], q_stride elements between rows (a multiple of 8)
- *   o  bf16 [n_rows][nq * 128], o_stride elements between rows (a multiple of 8)
+ *   o  bf16 [n_rows][nq * 128], o_stride elements between rows (a multiple of
+ *      8); may be q itself with the same stride
  *   lse  float [n_rows][nq] or NULL
  *   max_rows  no sequence has more rows than this, 1..16;
  *             max_rows * (nq / nkv) <= 64

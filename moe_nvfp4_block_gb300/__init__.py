@@ -475,6 +475,11 @@ def moe_lm_head_argmax(x_norm, W, tok, ws, best_logit=None, stream=None):
 
 def moe_lm_head_logits(x_norm, W, logits, ws, stream=None):
     """logits float32 [K, V]: every logit moe_lm_head_argmax chooses from."""
+    (K, H), dev = x_norm.shape, x_norm.device
+    _like(x_norm, torch.bfloat16, (K, H), "x_norm")
+    _like(W, torch.bfloat16, (W.shape[0], H), "W", dev)
+    _like(logits, torch.float32, (K, W.shape[0]), "logits", dev)
+    _workspace(ws, dev)
     _check(lib.moe_lm_head_logits(_ptr(x_norm), x_norm.shape[0], x_norm.shape[1], _ptr(W), W.shape[0], _ptr(logits),
                                   _ptr(ws), ws.numel(), _stream(stream)), "moe_lm_head_logits")
 
@@ -488,6 +493,12 @@ def _like(t, dtype, shape, what, device=None):
     if device is not None and t.device != device:
         raise ValueError(f"{what} is on {t.device}, not {device}")
     return t.data_ptr()
+
+
+def _workspace(ws, device):
+    if ws.get_device() != device.index or not ws.is_contiguous():
+        raise ValueError(f"the workspace must be a contiguous tensor on {device}")
+    return ws.data_ptr(), ws.numel()
 
 
 class PagedKV:
@@ -559,6 +570,8 @@ def _starts(kv, row_start):
 def _call(what, device, stream, f, *args):
     """f(*args, stream) on the tensors' device, on its current stream if none is given."""
     i = device.index
+    if device.type != "cuda":
+        raise ValueError(f"{what} works on CUDA tensors, not on {device}")
     s = torch._C._cuda_getCurrentRawStream(i) if stream is None else stream.cuda_stream
     if torch._C._cuda_getDevice() == i:
         status = f(*args, s)
@@ -591,7 +604,7 @@ def moe_paged_kv_append(kv: PagedKV, k_new, v_new, row_start, ws, q=None, q_out=
         qp, qs = _strided(q, "q", kv, T, nq * 128)
         op, os_ = _strided(q_out, "q_out", kv, T, nq * 128)
     _call("moe_paged_kv_append", kv.device, stream, lib.moe_paged_kv_append, kv._ref, qp, qs, kp, ks, vp, vs, T, nq,
-          _starts(kv, row_start), None if pos is None else ctypes.byref(pos), op, os_, ws.data_ptr(), ws.numel())
+          _starts(kv, row_start), None if pos is None else ctypes.byref(pos), op, os_, *_workspace(ws, kv.device))
 
 
 def moe_paged_attention(kv: PagedKV, q, row_start, o, ws, max_rows, scores: PagedScores | None = None, lse=None,
@@ -609,7 +622,7 @@ def moe_paged_attention(kv: PagedKV, q, row_start, o, ws, max_rows, scores: Page
         ref = scores._ref
     lp = _like(lse, torch.float32, (T, nq), "lse", kv.device)
     _call("moe_paged_attention", kv.device, stream, lib.moe_paged_attention, kv._ref, qp, qs, T, max_rows, nq,
-          _starts(kv, row_start), ref, op, os_, lp, ws.data_ptr(), ws.numel())
+          _starts(kv, row_start), ref, op, os_, lp, *_workspace(ws, kv.device))
 
 
 class LogitRules:
@@ -635,6 +648,10 @@ class LogitRules:
                 (torch.int32, torch.uint32) if n == "allow" else (torch.int32,)
             if t is not None and t.dtype not in want:
                 raise ValueError(f"{n} must be {want[0]}")
+        if any(t is not None and t.dim() != 2 for t in (bias, allow)) or (tokens is not None and tokens.numel() >= 2**31):
+            raise ValueError("bias and allow must be matrices, tokens fewer than 2^31")
+        if tokens is not None and tokens.numel() == 0:  # no history (an empty tensor has no address)
+            tokens = begin = end = None
         self.rows = rows.pop() if rows else None
         self.device = given[0].device if given else None
         p = lambda t: None if t is None else t.data_ptr()
@@ -671,8 +688,8 @@ def moe_logits_constrain(logits, rules: LogitRules | None, ws, out=None, tok=Non
     _call("moe_logits_constrain", dev, stream, lib.moe_logits_constrain, logits.data_ptr(),
           MOE_LOGITS_BF16 if logits.dtype == torch.bfloat16 else MOE_LOGITS_F32, logits.stride(0), R, V, ref,
           None if out is None else out.data_ptr(), 0 if out is None else out.stride(0),
-          _like(tok, torch.int32, (R,), "tok", dev), _like(best, torch.float32, (R,), "best", dev), ws.data_ptr(),
-          ws.numel())
+          _like(tok, torch.int32, (R,), "tok", dev), _like(best, torch.float32, (R,), "best", dev),
+          *_workspace(ws, dev))
 
 
 def moe_workspace_error(ws, stream=None) -> int:

@@ -70,8 +70,9 @@ moe_status paged_rows(const moe_paged_kv* kv, int n_rows, const int32_t* row_sta
   return MOE_OK;
 }
 
-// A row-strided bf16 matrix of `width` columns.
+// A row-strided bf16 matrix of `width` columns (no rows: anything).
 moe_status check_rows(const void* p, int64_t stride, int n_rows, int width) {
+  if (n_rows == 0) return MOE_OK;
   if (!p) return MOE_ERR_INVALID_ARG;
   if (!aligned16(p) || stride % 8 != 0) return MOE_ERR_MISALIGNED;
   if (n_rows > 1 && stride < width) return MOE_ERR_INVALID_ARG;
@@ -165,6 +166,7 @@ moe_status moe_paged_attention(const moe_paged_kv* kv, const uint16_t* q, int64_
   if ((st = check_rows(q, q_stride, n_rows, nq * 128)) != MOE_OK ||
       (st = check_rows(o, o_stride, n_rows, nq * 128)) != MOE_OK)
     return st;
+  if (q == o && q_stride != o_stride && n_rows > 1) return MOE_ERR_INVALID_ARG;
   if (!aligned4(lse)) return MOE_ERR_MISALIGNED;
   const moe_paged_scores none{};
   if (!scores) scores = &none;

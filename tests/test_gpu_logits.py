@@ -160,6 +160,52 @@ def test_more_repeated_tokens_than_a_list_holds(M, dtype):
                frequency=torch.rand(R, generator=g)))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_long_list_in_place(M, dtype):
+    # the stretches of a tile one after another, each over what it read
+    R, V = 700, 14001
+    g = torch.Generator().manual_seed(4)
+    d = rules_for(R, V, 5, history=1)
+    d["tokens"] = torch.cat([torch.randperm(V, generator=g), torch.randint(0, 9000, (5000,), generator=g)]).int()
+    d["begin"] = torch.tensor([(r * 41) % 3000 for r in range(R)], dtype=torch.int32)
+    d["end"] = torch.tensor([len(d["tokens"]) - (r % 7) * 900 for r in range(R)], dtype=torch.int32)
+    check(M, torch.randn(R, V, generator=g).to(dtype), d, in_place=True)
+
+
+def test_whole_rows_of_a_large_vocabulary(M):
+    # as many rows as SMs and more: a CTA takes up to 131,072 tokens
+    R, V = 256, 128003
+    g = torch.Generator().manual_seed(6)
+    d = rules_for(R, V, 7, history=40)
+    d["end"][::5] = d["begin"][::5].clamp(min=0) + 9000
+    check(M, torch.randn(R, V, generator=g).bfloat16(), d)
+    check(M, torch.randn(R, V, generator=g).bfloat16(), d, in_place=True)
+
+
+def test_an_empty_history(M):
+    x = torch.randn(3, 900, generator=torch.Generator().manual_seed(1))
+    e = torch.zeros(0, dtype=torch.int32)
+    check(M, x, dict(tokens=e, begin=torch.zeros(3, dtype=torch.int32), end=torch.ones(3, dtype=torch.int32),
+                     repetition=torch.full((3,), 2.0)))
+
+
+def test_two_streams_at_once(M):
+    xs = [torch.randn(40, 30011, device="cuda") for _ in range(2)]
+    d = [rules_for(40, 30011, s) for s in (1, 2)]
+    rules = [M.LogitRules(**{k: v.cuda() for k, v in q.items()}) for q in d]
+    ws, outs = [M.logits_workspace(40, 30011) for _ in xs], [torch.empty_like(x) for x in xs]
+    toks = [torch.empty(40, dtype=torch.int32, device="cuda") for _ in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i in range(2):
+            M.moe_logits_constrain(xs[i], rules[i], ws[i], out=outs[i], tok=toks[i], stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        want, wtok, _ = ref.logits(xs[i].cpu(), **d[i])
+        assert torch.equal(outs[i].cpu(), want) and torch.equal(toks[i].cpu(), wtok)
+
+
 def test_rows_past_the_tables_are_recorded(M):
     R, V = 3, 900
     x = torch.randn(R, V, generator=torch.Generator().manual_seed(1))

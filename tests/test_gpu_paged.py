@@ -252,6 +252,76 @@ def test_another_stream(M):
     assert torch.equal(o, o2)
 
 
+@pytest.mark.parametrize("nq,rows", [(8, [2, 1]), (8, [8, 5]), (8, [16, 9])])
+def test_output_over_the_queries(M, nq, rows):
+    lens = [5000, 40]
+    k, v, table, n, start = ref.make_cache(lens, rows, 2, 64, 0)
+    q = queries(sum(rows), nq, 1)
+    o, lse, ws = run(M, k, v, table, n, start, q, nq, 16)
+    kv, got = M.PagedKV(k, v, table, n), q.clone()
+    M.moe_paged_attention(kv, got, start, got, ws, 16)
+    assert torch.equal(got, o)
+
+
+def test_no_rows(M):
+    k, v, table, n, start = ref.make_cache([5], [0], 2, 16, 0)
+    kv = M.PagedKV(k, v, table, n)
+    ws, q = M.paged_workspace(kv, 1, 4), queries(0, 4, 1)
+    M.moe_paged_kv_append(kv, queries(0, 2, 2), queries(0, 2, 3), start, ws, q=q, q_out=q)
+    M.moe_paged_attention(kv, q, start, q, ws, 1)
+    assert M.moe_workspace_error(ws) == 0
+
+
+@pytest.mark.parametrize("nq,rows", [(8, [2, 1]), (8, [16, 9])])
+def test_two_streams_at_once(M, nq, rows):
+    lens = [[6000, 300], [100, 9000]]
+    caches = [ref.make_cache(l, rows, 2, 64, i) for i, l in enumerate(lens)]
+    kvs, qs = [M.PagedKV(*c[:4]) for c in caches], [queries(sum(rows), nq, i) for i in range(2)]
+    ws, os_ = [M.paged_workspace(kv, 16, nq) for kv in kvs], [torch.empty_like(q) for q in qs]
+    streams = [torch.cuda.Stream() for _ in kvs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in range(2):
+            M.moe_paged_attention(kvs[i], qs[i], caches[i][4], os_[i], ws[i], 16, stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        k, v, table = caches[i][:3]
+        ref.check_attention(os_[i], None, ref.attention(qs[i], k, v, table, lens[i], rows, nq))
+
+
+def test_a_captured_step_appends_and_attends(M):
+    # append, attention and commit as one graph: each replay sees what the one before appended
+    lens, K, nq, nkv, ps = [60, 3, 250], 3, 8, 2, 64
+    k, v, table, n, start = ref.make_cache([l + 5 * K for l in lens], [K] * 3, nkv, ps, 0)
+    n.copy_(ints(lens))
+    kv, pos = M.PagedKV(k, v, table, n), M.attn_pos(rotary_dim=128)
+    qkv = queries(3 * K, nq + 2 * nkv, 1)
+    a, b = nq * HD, (nq + nkv) * HD
+    q, o, ws = torch.empty(3 * K, a, dtype=torch.bfloat16, device="cuda"), torch.empty(3 * K, a, dtype=torch.bfloat16, device="cuda"), \
+        M.paged_workspace(kv, K, nq)
+    step = lambda: (M.moe_paged_kv_append(kv, qkv[:, a:b], qkv[:, b:], start, ws, q=qkv[:, :a], q_out=q, pos=pos),
+                    M.moe_paged_attention(kv, q, start, o, ws, K))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for i in range(4):
+        qkv.normal_()
+        n.copy_(ints([l + i * K for l in lens]))
+        g.replay()
+        torch.cuda.synchronize()
+        ref.check_attention(o, None, ref.attention(q, k, v, table, [l + i * K for l in lens], [K] * 3, nq))
+        for s, l in enumerate(lens):  # the values as they came
+            for j in range(K):
+                p = l + i * K + j
+                assert torch.equal(v[table[s, p // ps].long(), :, p % ps].flatten(), qkv[s * K + j, b:])
+    assert M.moe_workspace_error(ws) == 0
+
+
 def test_offsets_past_32_bits(M):
     # a pool of 2^31 + elements: the last pages lie past 2^32 bytes and 2^31 elements
     nkv, ps = 8, 128

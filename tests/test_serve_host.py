@@ -93,6 +93,41 @@ def test_no_rows_is_no_work(M):
     assert append(M, n=0) == OK and attention(M, n=0) == OK
 
 
+def test_no_rows_need_no_matrices(M):
+    # an empty tensor has no address
+    assert append(M, n=0, q=None, qo=None, k=None, v=None) == OK and attention(M, n=0, q=None, o=None) == OK
+
+
+def test_output_over_the_queries_wants_their_stride(M):
+    assert attention(M, q=16, o=16, os_=4104) == INVALID
+
+
+def test_binding_refuses_rules_it_would_misread(M):
+    with pytest.raises(ValueError):
+        M.LogitRules(bias=torch.zeros(50), bias_row=torch.zeros(3, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        M.LogitRules(allow=torch.zeros(2, dtype=torch.int32), allow_row=torch.zeros(3, dtype=torch.int32))
+    empty, row = torch.zeros(0, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    c = M.LogitRules(tokens=empty, begin=row, end=row, repetition=torch.ones(3)).c
+    assert c.tokens is None and c.begin is None and c.end is None
+
+
+def test_binding_refuses_tensors_of_the_wrong_place(M):
+    bf, i32 = torch.bfloat16, torch.int32
+    k, table, n = torch.zeros(6, 2, 16, 128, dtype=bf), torch.zeros(3, 2, dtype=i32), torch.zeros(3, dtype=i32)
+    c, rows, start, ws = M.PagedKV(k, k.clone(), table, n), torch.zeros(5, 256, dtype=bf), torch.zeros(4, dtype=i32), \
+        torch.zeros(1 << 20, dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        M.moe_paged_kv_append(c, rows, rows, start, ws)
+    with pytest.raises(ValueError):
+        M.moe_paged_attention(c, rows, start, rows, ws, 2)
+    w = torch.zeros(30, 256, dtype=bf)
+    for bad in (dict(logits=torch.zeros(5, 30, dtype=bf)), dict(logits=torch.zeros(4, 30)), dict(W=w.float()),
+                dict(W=w[:, :128]), dict(x_norm=rows.float()), dict(logits=torch.zeros(30, 5).T)):
+        with pytest.raises(ValueError):
+            M.moe_lm_head_logits(**(dict(x_norm=rows, W=w, logits=torch.zeros(5, 30), ws=ws) | bad))
+
+
 def test_paged_workspace_sizes(M):
     f = M.lib.moe_paged_workspace_size
     assert f(0, 32, 8) == 0 and f(17, 8, 8) == 0 and f(2, 12, 8) == 0 and f(16, 64, 8) == 0 and f(1, 8, 0) == 0
