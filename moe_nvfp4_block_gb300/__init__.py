@@ -511,7 +511,7 @@ class PagedKV:
         n, nkv, ps, hd = kpages.shape
         dev = kpages.device
         self.kpages, self.vpages, self.table, self.kv_len, self.device = kpages, vpages, table, kv_len, dev
-        self.nkv, self.n_seqs = nkv, kv_len.shape[0]
+        self.nkv, self.n_seqs, self.index = nkv, kv_len.shape[0], kpages.get_device()
         self.c = moe_paged_kv(_like(kpages, torch.bfloat16, (n, nkv, ps, hd), "kpages"),
                               _like(vpages, torch.bfloat16, (n, nkv, ps, hd), "vpages", dev),
                               _like(table, torch.int32, (kv_len.shape[0], table.shape[1]), "table", dev),
@@ -552,17 +552,18 @@ def paged_workspace(kv: PagedKV, max_rows: int, nq: int) -> torch.Tensor:
 
 def _strided(t, what, kv, n_rows, width=None):
     """(address, row stride) of a row-strided bf16 matrix [n_rows, heads * 128]."""
-    if (t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[0] != n_rows or (width and t.shape[1] != width)
-            or t.stride(1) != 1 or t.device != kv.device):
+    shape, stride = t.shape, t.stride()
+    if (t.dtype is not torch.bfloat16 or len(shape) != 2 or shape[0] != n_rows or (width and shape[1] != width)
+            or stride[1] != 1 or t.get_device() != kv.index):
         raise ValueError(f"{what} must be a bf16 tensor [{n_rows}, {width or 'heads * 128'}] with unit column stride "
                          f"on {kv.device}")
-    return t.data_ptr(), t.stride(0)
+    return t.data_ptr(), stride[0]
 
 
 def _starts(kv, row_start):
     n = kv.n_seqs + 1
-    if row_start.dtype != torch.int32 or row_start.shape != (n,) or row_start.device != kv.device or \
-            not row_start.is_contiguous():
+    if (row_start.dtype is not torch.int32 or row_start.shape != (n,) or row_start.get_device() != kv.index
+            or not row_start.is_contiguous()):
         raise ValueError(f"row_start must be an int32 tensor [{n}] on {kv.device}")
     return row_start.data_ptr()
 
