@@ -22,9 +22,9 @@ namespace moe {
 
 namespace {
 
-constexpr int kLlWarps = 12;
+constexpr int kLlWarps = 8;
 constexpr int kLlSlots = 2;
-constexpr int kLlRows = 4;      // vocab rows of a warp's step
+constexpr int kLlRows = 8;      // vocab rows of a warp's step
 constexpr int kLlCols = 512;    // columns of a slot
 constexpr int kLlSlotBytes = kLlRows * kLlCols * 2;
 constexpr uint64_t kLlDrainNs = 2000000000ull;
@@ -78,10 +78,11 @@ __global__ void __launch_bounds__(kLlWarps * 32, 1) k_lmhead_logits(const __grid
   const int g0 = warp * gridDim.x + blockIdx.x;  // this warp's groups of rows: g0, g0 + step, ...
   const int nst = g0 < ngrp ? ((ngrp - 1 - g0) / step + 1) * nblk : 0;
   volatile int* abort = &T.abort;
-  // stage s: column block s % nblk of the group g0 + (s / nblk) step
+  // stage s: column block s % nblk of the group g0 + (s / nblk) step, asked for
+  // in order, by the whole warp, a row a lane
   const uint64_t pol = policy_evict_first();
-  auto issue = [&](int s) {  // by the whole warp, a row a lane
-    const int grp = g0 + s / nblk * step, c0 = s % nblk * kLlCols;
+  int grp = g0, c0 = 0;
+  auto issue = [&](int s) {
     const uint32_t bytes = (uint32_t)min(kLlCols, H - c0) * 2u;
     const int nr = min(kLlRows, V - grp * kLlRows);
     uint64_t* bar = &T.full[warp][s % kLlSlots];
@@ -90,6 +91,10 @@ __global__ void __launch_bounds__(kLlWarps * 32, 1) k_lmhead_logits(const __grid
     if (lane < nr)
       bulk_load(ring + (size_t)(s % kLlSlots) * kLlSlotBytes + lane * (kLlCols * 2),
                 a.W + (size_t)(grp * kLlRows + lane) * H + c0, bytes, bar, pol);
+    if ((c0 += kLlCols) >= H) {
+      c0 = 0;
+      grp += step;
+    }
   };
   if (lane == 0) {
     for (int i = 0; i < kLlSlots; ++i) mbar_init(&T.full[warp][i], 1);
@@ -110,9 +115,8 @@ __global__ void __launch_bounds__(kLlWarps * 32, 1) k_lmhead_logits(const __grid
   __syncthreads();
 
   unsigned long long acc[kLlRows][KR / 2];  // {row 2p, row 2p + 1} of vocab row q
-  int s = 0;
+  int s = 0, blk = 0, v0 = g0 * kLlRows;
   for (; s < nst; ++s) {
-    const int blk = s % nblk;
     bool ok = !*abort && mbar_wait_bounded(&T.full[warp][s % kLlSlots], (uint32_t)(s / kLlSlots) & 1u, a.wait_ns, abort);
     if (!__all_sync(0xffffffffu, ok)) {
       *abort = 1;
@@ -158,23 +162,25 @@ __global__ void __launch_bounds__(kLlWarps * 32, 1) k_lmhead_logits(const __grid
     }
     __syncwarp();
     if (s + kLlSlots < nst) issue(s + kLlSlots);
-    if (blk != nblk - 1) continue;
-    // sums b = q + 4 r of rows r = 8 h .. 8 h + 7, one a lane
-    const int v0 = (g0 + s / nblk * step) * kLlRows;
+    if (++blk < nblk) continue;
+    blk = 0;
+    // sums b = q + kLlRows r of 32 / kLlRows rows of x at a time, one a lane
+    constexpr int RB = 32 / kLlRows;
 #pragma unroll
-    for (int h = 0; h < KR / 8; ++h) {
+    for (int h = 0; h < KR / RB; ++h) {
       float v[32];
 #pragma unroll
       for (int b = 0; b < 32; ++b) {
-        const int r = 8 * h + (b >> 2);
+        const int r = RB * h + b / kLlRows;
         float lo, hi;
-        asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(acc[b & 3][r >> 1]));
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(acc[b % kLlRows][r >> 1]));
         v[b] = (r & 1) ? hi : lo;
       }
       const float l = ll_reduce32(v, lane);
-      const int r = 8 * h + (lane >> 2), q = lane & 3;
+      const int r = RB * h + lane / kLlRows, q = lane % kLlRows;
       if (r < K && v0 + q < V) a.logits[(size_t)r * V + v0 + q] = l;
     }
+    v0 += step * kLlRows;
   }
   if (*abort && s < nst) {
     // this warp's copies still in flight (those of stage s on) land before it leaves
