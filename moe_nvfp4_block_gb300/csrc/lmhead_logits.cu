@@ -4,17 +4,25 @@
 // 16, 8, 4, 2, 1.
 //
 // What bounds it: that order leaves the products to the FP32 units (K H V
-// multiply-adds at 128 an SM and clock: 14 us at K 16, H 1024, V 32,003, where
-// the weights' own bytes take 10).  So the other instructions have to be few:
-//  * a warp takes four vocab rows and two rows of x at a time: one
+// multiply-adds at 128 an SM and clock: 131 us at K 16, H 2048, V 151,936,
+// where the weights' own bytes take 92, and it takes 212; at K 8 it takes 125,
+// at K 16, H 1024 and V 32,003 31, where the products take 14).  So the other
+// instructions have to be few:
+//  * a warp takes eight vocab rows and two rows of x at a time: one
 //    fma.rn.f32x2 (two correctly rounded multiply-adds, so the same bits) per
-//    pair of rows, with the weight in both halves;
+//    pair of rows, with the weight in both halves; x, its rows' bf16 side by
+//    side in a word, is unpacked once for eight rows (four rows and half as
+//    many registers, twelve warps: 262 us; rows apart: 233);
+//  * eight warps hold the sums of 16 rows, twelve those of 8 (144 us with
+//    eight; ten, uneven over the four schedulers, 151; an earlier form);
+//  * slots of 512 columns (of 256: 287 us), counted without divisions (221 and
+//    235 us, an earlier form);
 //  * the xor rounds of 32 (row, vocab) sums together: in each round a lane
 //    hands over the half of its sums that its partner keeps, 31 shuffles for
 //    32 sums instead of 160 (a + b = b + a, so again the same bits), and lane
 //    b ends with sum b.
-// Each warp streams its own weights through two 4 KB slots (four rows x up to
-// 512 columns, one bulk copy a row) and waits for no other warp.
+// Each warp streams its own weights through two 8 KB slots (one bulk copy a
+// row) and waits for no other warp.
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -22,15 +30,17 @@ namespace moe {
 
 namespace {
 
-constexpr int kLlWarps = 8;
 constexpr int kLlSlots = 2;
 constexpr int kLlRows = 8;      // vocab rows of a warp's step
 constexpr int kLlCols = 512;    // columns of a slot
 constexpr int kLlSlotBytes = kLlRows * kLlCols * 2;
 constexpr uint64_t kLlDrainNs = 2000000000ull;
 
+// The warps of an SM, by the registers of their KR x kLlRows sums.
+__host__ __device__ constexpr int ll_warps(int KR) { return KR == 8 ? 12 : 8; }
+
 struct LlTable {
-  uint64_t full[kLlWarps][kLlSlots];
+  uint64_t full[12][kLlSlots];
   int abort;
 };
 
@@ -66,12 +76,13 @@ __device__ __forceinline__ float ll_reduce32(float (&v)[32], int lane) {
 }  // namespace
 
 template <int KR>
-__global__ void __launch_bounds__(kLlWarps * 32, 1) k_lmhead_logits(const __grid_constant__ LmHeadArgs a) {
+__global__ void __launch_bounds__(ll_warps(KR) * 32, 1) k_lmhead_logits(const __grid_constant__ LmHeadArgs a) {
+  constexpr int kLlWarps = ll_warps(KR);
   extern __shared__ __align__(128) unsigned char smem[];
   const int K = a.K, H = a.H, V = a.V;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   unsigned char* ring = smem + (size_t)warp * kLlSlots * kLlSlotBytes;
-  uint2* xs = reinterpret_cast<uint2*>(smem + (size_t)kLlWarps * kLlSlots * kLlSlotBytes);  // [KR][H] bf16
+  uint4* xs = reinterpret_cast<uint4*>(smem + (size_t)kLlWarps * kLlSlots * kLlSlotBytes);  // [KR][H] bf16
   LlTable& T = *reinterpret_cast<LlTable*>(reinterpret_cast<unsigned char*>(xs) + (size_t)KR * H * 2);
   const int nblk = (H + kLlCols - 1) / kLlCols;
   const int ngrp = (V + kLlRows - 1) / kLlRows, step = gridDim.x * kLlWarps;
@@ -104,13 +115,18 @@ __global__ void __launch_bounds__(kLlWarps * 32, 1) k_lmhead_logits(const __grid
   __syncthreads();
   for (int s = 0; s < min(nst, kLlSlots); ++s) issue(s);
   pdl_launch_dependents();
-  // x in planes [row][256 columns][first or second half of a lane's eight][lane][4]:
-  // a warp's 8-byte reads are consecutive (all banks)
-  for (int i = threadIdx.x; i < KR * H / 8; i += blockDim.x) {
-    const uint4 v = i < K * H / 8 ? __ldcg(reinterpret_cast<const uint4*>(a.x) + i) : make_uint4(0u, 0u, 0u, 0u);
-    uint2* at = xs + (size_t)(i >> 5) * 64 + (i & 31);
-    at[0] = make_uint2(v.x, v.y);
-    at[32] = make_uint2(v.z, v.w);
+  // x in planes [pair of rows][256 columns][first or second half of a lane's
+  // eight][lane][4 words {row 2p, row 2p + 1}]: a warp's 16-byte reads are consecutive
+  for (int i = threadIdx.x; i < KR / 2 * H / 8; i += blockDim.x) {
+    const int p = i / (H / 8), c = i - p * (H / 8);
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    const uint4* x = reinterpret_cast<const uint4*>(a.x) + (size_t)2 * p * (H / 8) + c;
+    const uint4 u = 2 * p < K ? __ldcg(x) : z, v = 2 * p + 1 < K ? __ldcg(x + H / 8) : z;
+    uint4* at = xs + (size_t)(i >> 5) * 64 + (i & 31);
+    at[0] = make_uint4(__byte_perm(u.x, v.x, 0x5410), __byte_perm(u.x, v.x, 0x7632), __byte_perm(u.y, v.y, 0x5410),
+                       __byte_perm(u.y, v.y, 0x7632));
+    at[32] = make_uint4(__byte_perm(u.z, v.z, 0x5410), __byte_perm(u.z, v.z, 0x7632), __byte_perm(u.w, v.w, 0x5410),
+                        __byte_perm(u.w, v.w, 0x7632));
   }
   __syncthreads();
 
@@ -135,7 +151,7 @@ __global__ void __launch_bounds__(kLlWarps * 32, 1) k_lmhead_logits(const __grid
       uint4 w[kLlRows];
 #pragma unroll
       for (int q = 0; q < kLlRows; ++q) w[q] = ws[q * (kLlCols / 8) + j * 32 + lane];
-      const uint2* xj = xs + (blk * (kLlCols / 256) + j) * 64 + lane;
+      const uint4* xj = xs + (blk * (kLlCols / 256) + j) * 64 + lane;
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {  // elements 0-3, 4-7 of the lane's eight
         unsigned long long ww[kLlRows][4];
@@ -148,14 +164,13 @@ __global__ void __launch_bounds__(kLlWarps * 32, 1) k_lmhead_logits(const __grid
           }
 #pragma unroll
         for (int p = 0; p < KR / 2; ++p) {
-          const uint2 x0 = xj[2 * p * (H / 4) + 32 * hf], x1 = xj[(2 * p + 1) * (H / 4) + 32 * hf];
+          const uint4 x = xj[p * (H / 4) + 32 * hf];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t u0 = i < 2 ? x0.x : x0.y, u1 = i < 2 ? x1.x : x1.y;
-            const unsigned long long xx = (i & 1) ? ll_pair(__uint_as_float(u0 & 0xFFFF0000u), __uint_as_float(u1 & 0xFFFF0000u))
-                                                  : ll_pair(__uint_as_float(u0 << 16), __uint_as_float(u1 << 16));
+            const uint32_t u = i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
+            const unsigned long long xx = ll_pair(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
 #pragma unroll
-            for (int q = 0; q < kLlRows; ++q) ll_fma2(acc[q][p], xx, ww[q][i]);
+            for (int q = 0; q < kLlRows; ++q) ll_fma2(acc[q][p], ww[q][i], xx);
           }
         }
       }
@@ -194,6 +209,7 @@ __global__ void __launch_bounds__(kLlWarps * 32, 1) k_lmhead_logits(const __grid
 
 template <int KR>
 static cudaError_t launch_lmhead_logits_t(const LmHeadArgs& a, cudaStream_t s) {
+  constexpr int kLlWarps = ll_warps(KR);
   const size_t sm = (size_t)kLlWarps * kLlSlots * kLlSlotBytes + (size_t)KR * a.H * 2 + sizeof(LlTable);
   constexpr int most = kLlWarps * kLlSlots * kLlSlotBytes + KR * 2048 * 2 + (int)sizeof(LlTable);
   const cudaError_t e = prepare_kernel<k_lmhead_logits<KR>>(most);
