@@ -489,7 +489,9 @@ size_t moe_paged_workspace_size(int max_rows, int nq, int nkv);
  *              fused projection's output need no copy)
  * The rotation is the attention block's: the angle reduced in double, sine
  * and cosine in FP32, each product and sum rounded to FP32, one bf16
- * rounding at the end.
+ * rounding at the end.  (YaRN's temperature, which the attention block puts
+ * into its scale, (0.1 ln yarn_factor + 1)^2 / sqrt(128), is the caller's to
+ * put into moe_paged_scores.)
  * A row whose position has no page (MOE_ERR_CAPACITY) or a page id out of
  * range is not stored; its query is turned all the same.
  */

@@ -450,7 +450,7 @@ static moe_status lm_head_impl(const uint16_t* x_norm, int K, int H, const uint1
   a.wait_ns = g_wait_ns.load();
   a.logits = logits;
   cudaError_t e;
-  if (logits && K > 4) {
+  if (logits) {
     e = launch_lmhead_logits(a, static_cast<cudaStream_t>(stream));
   } else if (lmhead_stream_fits(K, H)) {
     e = launch_lmhead_stream(a, static_cast<cudaStream_t>(stream), pdl);

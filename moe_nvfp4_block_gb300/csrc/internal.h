@@ -311,7 +311,7 @@ cudaError_t launch_rmsnorm(const uint16_t* x, int K, int H, float eps, uint16_t*
 cudaError_t launch_lmhead(const LmHeadArgs& a, cudaStream_t s, bool pdl);
 bool lmhead_stream_fits(int K, int H);
 cudaError_t launch_lmhead_stream(const LmHeadArgs& a, cudaStream_t s, bool pdl);
-cudaError_t launch_lmhead_logits(const LmHeadArgs& a, cudaStream_t s);  // K > 4, H <= 2048
+cudaError_t launch_lmhead_logits(const LmHeadArgs& a, cudaStream_t s);  // H <= 2048
 cudaError_t launch_router(const RouterArgs& a, cudaStream_t s, bool pdl);
 // One launch of the experts kernel: maps [kMapsPerLayer].
 cudaError_t launch_experts(const ExpertsCommon& c, const CUtensorMap* maps, const LayerDesc& desc, cudaStream_t s,

@@ -1,4 +1,4 @@
-// lmhead_logits.cu -- the lm_head's logits of 5 to 16 rows, bit for bit those
+// lmhead_logits.cu -- the lm_head's logits of 1 to 16 rows, bit for bit those
 // of the argmax kernels: lane l of a warp owns elements 256 j + 8 l + i and
 // accumulates them in element order, the 32 lane sums are added in xor rounds
 // 16, 8, 4, 2, 1.
@@ -13,7 +13,7 @@
 //    pair of rows, with the weight in both halves; x, its rows' bf16 side by
 //    side in a word, is unpacked once for eight rows (four rows and half as
 //    many registers, twelve warps: 262 us; rows apart: 233);
-//  * eight warps hold the sums of 16 rows, twelve those of 8 (144 us with
+//  * eight warps hold the sums of 16 rows, twelve those of 8 or 4 (K 8: 144 us with
 //    eight; ten, uneven over the four schedulers, 151; an earlier form);
 //  * slots of 512 columns (of 256: 287 us), counted without divisions (221 and
 //    235 us, an earlier form);
@@ -37,7 +37,7 @@ constexpr int kLlSlotBytes = kLlRows * kLlCols * 2;
 constexpr uint64_t kLlDrainNs = 2000000000ull;
 
 // The warps of an SM, by the registers of their KR x kLlRows sums.
-__host__ __device__ constexpr int ll_warps(int KR) { return KR == 8 ? 12 : 8; }
+__host__ __device__ constexpr int ll_warps(int KR) { return KR <= 8 ? 12 : 8; }
 
 struct LlTable {
   uint64_t full[12][kLlSlots];
@@ -223,9 +223,11 @@ static cudaError_t launch_lmhead_logits_t(const LmHeadArgs& a, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, k_lmhead_logits<KR>, a);
 }
 
-// More than 4 rows (fewer are bound by the weights' bytes: k_lmhead_stream).
+// Rows are padded to 4, 8 or 16.  Up to 4 the weights' bytes bound it, and K 1
+// takes what K 4 takes: 97 and 100 us at H 2048, V 151,936 (92 at the copy's
+// bandwidth), 15 at H 1024, V 32,003 (10).
 cudaError_t launch_lmhead_logits(const LmHeadArgs& a, cudaStream_t s) {
-  return a.K <= 8 ? launch_lmhead_logits_t<8>(a, s) : launch_lmhead_logits_t<16>(a, s);
+  return a.K <= 4 ? launch_lmhead_logits_t<4>(a, s) : a.K <= 8 ? launch_lmhead_logits_t<8>(a, s) : launch_lmhead_logits_t<16>(a, s);
 }
 
 }  // namespace moe

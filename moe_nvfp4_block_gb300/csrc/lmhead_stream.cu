@@ -66,8 +66,7 @@ template <int KR> struct LsShape {
 
 }  // namespace
 
-// LOGITS (K <= 4): every logit is stored (a.logits) and no argmax taken.
-template <int KR, bool LOGITS>
+template <int KR>
 __global__ void __launch_bounds__(2 * LsShape<KR>::pairs * 32, 1) k_lmhead_stream(const __grid_constant__ LmHeadArgs a) {
   constexpr int kLsPairs = LsShape<KR>::pairs, kLsWarps = 2 * kLsPairs, kLsSlotBytes = LsShape<KR>::slot;
   constexpr int RPW = LsShape<KR>::rpw;
@@ -256,9 +255,7 @@ __global__ void __launch_bounds__(2 * LsShape<KR>::pairs * 32, 1) k_lmhead_strea
           for (int r = 0; r < KR; ++r) {
             if (r < K) {
               const float l = lsum_xor(acc[q][r]);
-              if constexpr (LOGITS) {
-                if (lane == r) a.logits[(size_t)r * V + vb + row] = l;
-              } else if (bi[r] == INT_MAX || l > bv[r]) {  // this warp's rows arrive in increasing order
+              if (bi[r] == INT_MAX || l > bv[r]) {  // this warp's rows arrive in increasing order
                 bv[r] = l;
                 bi[r] = vb + row;
               }
@@ -275,7 +272,6 @@ __global__ void __launch_bounds__(2 * LsShape<KR>::pairs * 32, 1) k_lmhead_strea
     if (hw == 0 && lane == 0 && issued > 0) mbar_wait_drain(&T.full[p], (uint32_t)(issued - 1) & 1u, kLsDrainNs);
     if (threadIdx.x == 0 && a.err) atomicCAS(a.err, 0, (int)MOE_ERR_DEVICE_TIMEOUT);
   }
-  if constexpr (LOGITS) return;
   if (lane == 0) {
 #pragma unroll
     for (int r = 0; r < KR; ++r) {
@@ -354,10 +350,9 @@ cudaError_t launch_lmhead_stream(const LmHeadArgs& a0, cudaStream_t s, bool pdl)
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, a);
   };
-  if (a0.logits) return run(k_lmhead_stream<4, true>, LsShape<4>::pairs, LsShape<4>::slot, LsShape<4>::rpw);
-  if (a0.K <= 4) return run(k_lmhead_stream<4, false>, LsShape<4>::pairs, LsShape<4>::slot, LsShape<4>::rpw);
-  if (a0.K <= 8) return run(k_lmhead_stream<8, false>, LsShape<8>::pairs, LsShape<8>::slot, LsShape<8>::rpw);
-  return run(k_lmhead_stream<16, false>, LsShape<16>::pairs, LsShape<16>::slot, LsShape<16>::rpw);
+  if (a0.K <= 4) return run(k_lmhead_stream<4>, LsShape<4>::pairs, LsShape<4>::slot, LsShape<4>::rpw);
+  if (a0.K <= 8) return run(k_lmhead_stream<8>, LsShape<8>::pairs, LsShape<8>::slot, LsShape<8>::rpw);
+  return run(k_lmhead_stream<16>, LsShape<16>::pairs, LsShape<16>::slot, LsShape<16>::rpw);
 }
 
 }  // namespace moe

@@ -12,6 +12,15 @@ pytestmark = pytest.mark.gpu
 HD = 128
 
 
+@pytest.fixture(autouse=True)
+def fp32_default():
+    """The files of a run share torch's default type."""
+    old = torch.get_default_dtype()
+    torch.set_default_dtype(torch.float32)
+    yield
+    torch.set_default_dtype(old)
+
+
 @pytest.fixture(scope="module")
 def M(cuda_ok):
     import moe_nvfp4_block_gb300 as M

@@ -8,6 +8,15 @@ import torch
 OK, INVALID, SHAPE, WORKSPACE, ALIGN = 0, -1, -2, -3, -4
 
 
+@pytest.fixture(autouse=True)
+def fp32_default():
+    """The files of a run share torch's default type."""
+    old = torch.get_default_dtype()
+    torch.set_default_dtype(torch.float32)
+    yield
+    torch.set_default_dtype(old)
+
+
 @pytest.fixture(scope="module")
 def M():
     import __graft_entry__
