@@ -65,8 +65,8 @@ struct TcTable {
   uint64_t p_full[2];   // P of group g is there
   uint64_t o_done[2];   // the product with P of group g is done
   uint64_t q_full, q_empty;  // the segment's Q is there; its last product with it is done
-  uint64_t ml_full;     // the segment's m and l are there
-  uint64_t epi_done;    // the segment's outputs are out of tensor memory (a group's first P of the next waits)
+  uint64_t ml_full;     // m and l of a segment of both groups are there
+  uint64_t epi_done;    // its outputs are out of tensor memory (a group's first P of the next segment waits)
   uint64_t fin[2];
   uint32_t tmem;
   int pv[2];            // slices to multiply (bits 0-3); bit 4: O holds sums already
@@ -128,6 +128,22 @@ __device__ __forceinline__ void tc_st32(uint32_t t, const uint32_t* r) {
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
       "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+// 16 columns.
+__device__ __forceinline__ void tc_ld16(uint32_t t, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(t)
+      : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t t, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(t),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -388,7 +404,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
     const uint32_t t_s = tmem + t_lane + kTcS + 32 * half, t_o = tmem + t_lane + kTcO + 128 * g;
     const uint32_t p_row = smem_addr(s_p) + g * kTcP + row * 128;
     uint32_t xpar = 0;
+    const float unit = a.plain ? a.scale_log2 : 1.f;
     bool ok = true;
+    int shared = 0, cleared = 0;  // segments of both groups so far, those whose end has been waited for
     // the group's four warps: what each wrote before is there for all after
     auto exchange = [&]() {
       __syncwarp();
@@ -403,11 +421,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
       const TcSeg& D = T.seg[seg % kTcSegs];
       const int st0 = D.st0, st1 = st0 + D.count;
       if (st0 == st1) break;
+      const bool solo = st1 - st0 == 1;  // a segment of one chunk is its group's alone
+      if (solo && (st0 & 1) != g) {
+        done(seg);
+        continue;
+      }
       float m = -INFINITY, l = 0.f, slope = 0.f;
-      bool has = false, clean = seg == 0;  // clean: the last segment's outputs are out
+      bool has = false;
+      // the last shared segment's outputs are out
       auto cleaned = [&]() {
-        if (!clean) ok = wait(&T.epi_done, (uint32_t)(seg - 1) & 1u);
-        clean = true;
+        if (cleared != shared) ok = wait(&T.epi_done, (uint32_t)(shared - 1) & 1u);
+        cleared = shared;
         return ok;
       };
       const bool live = row < D.n * a.group;
@@ -434,19 +458,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&T.s_empty[st & 3]);
+        // in units of 1 / unit (log2 domain); plain scores are scaled with the exponential
         float s[32];
-        if (a.plain) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) s[c] = __uint_as_float(sr[c]) * a.scale_log2;
-        } else {
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
+        for (int c = 0; c < 32; ++c) s[c] = __uint_as_float(sr[c]);
+        if (!a.plain) {
+          if (a.cap_log2 > 0.f) {
             // tanh(z) = 1 - 2 / (e^2z + 1): off by an FP32 rounding of 1, an
             // absolute error, which is what a score needs
-            const float q = __uint_as_float(sr[c]);
-            float x = q * a.scale_log2;
-            if (a.cap_log2 > 0.f) x = a.cap_log2 * (1.f - 2.f * rcp(ex2(q * a.cap_in) + 1.f));
-            s[c] = x + slope * (float)(pos0 + 32 * half + c - rp);
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              s[c] = __fmaf_rn(-2.f * a.cap_log2, rcp(ex2(s[c] * a.cap_in) + 1.f), a.cap_log2);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) s[c] *= a.scale_log2;
+          }
+          if (a.slopes) {
+            const float d = (float)(pos0 + 32 * half - rp);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) s[c] = __fmaf_rn(slope, d + (float)c, s[c]);
           }
         }
         unsigned long long see = ~0ull;
@@ -464,7 +494,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
         if (!cleaned()) break;
         float(&s_top)[2][64] = T.top[own & 1][g];
         int(&s_odd)[4] = T.odd[own & 1][g];
-        s_top[half][row] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const float mine_top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        s_top[half][row] = mine_top;
         const uint32_t v0 = smem_addr(ring + (size_t)sl * kPaStageBytes + kPaHalf);
         if (any & ~clear) {
           // slices with hidden positions: infinite or NaN values among them?
@@ -491,7 +522,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
           if (lane == 0) s_odd[warp & 3] = odd;
         }
         if (!(ok = exchange())) break;
-        const float top = fmaxf(s_top[0][row], s_top[1][row]);
+        const float top = unit * fmaxf(mine_top, s_top[half ^ 1][row]);
         float scale = 1.f;
         if (top > m && (m == -INFINITY || top - m > kTcLazy)) {
           if (m != -INFINITY) scale = ex2(m - top);  // else the row's sums are zeros
@@ -502,7 +533,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
         float add[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < 32; ++c) {
-          s[c] = ex2(s[c] - ref);
+          s[c] = ex2(__fmaf_rn(s[c], unit, -ref));
           add[c & 3] += s[c];
         }
         l += (add[0] + add[1]) + (add[2] + add[3]);
@@ -512,13 +543,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
         tc_fence_after();
         if (half == 0 && has && __any_sync(0xffffffffu, scale != 1.f)) {
 #pragma unroll 1
-          for (int c = 0; c < 128; c += 32) {
-            uint32_t o[32];
-            tc_ld32(t_o + c, o);
+          for (int c = 0; c < 128; c += 16) {
+            uint32_t o[16];
+            tc_ld16(t_o + c, o);
             tc_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * scale);
-            tc_st32(t_o + c, o);
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * scale);
+            tc_st16(t_o + c, o);
           }
           tc_wait_st();
         }
@@ -585,6 +616,57 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
       }
       if (!ok) break;
       // ---------------------------------------------------------------- the segment's end
+      const bool whole = D.parts == 1;
+      const size_t prow = (size_t)(cta * 2 + D.slot) * rows + row;
+      // 16 dims of the row's output, or of this CTA's part of it
+      auto put = [&](int c, const float (&v)[16]) {
+        if (live && whole) {
+          uint4* out = reinterpret_cast<uint4*>(a.o + (D.q0 + r) * a.os + h * 128 + c);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            out[i] = make_uint4(pa_pack(v[8 * i], v[8 * i + 1]), pa_pack(v[8 * i + 2], v[8 * i + 3]),
+                                pa_pack(v[8 * i + 4], v[8 * i + 5]), pa_pack(v[8 * i + 6], v[8 * i + 7]));
+        } else if (live) {
+          float4* out = reinterpret_cast<float4*>(A.part_o + prow * 128 + c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) __stcg(out + i, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+        }
+      };
+      auto put_sums = [&](float M, float L) {
+        if (live && whole && a.lse)
+          a.lse[(size_t)(D.q0 + r) * a.nq + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+        if (live && !whole) __stcg(reinterpret_cast<float2*>(A.part_ml + 2 * prow), make_float2(M, L));
+        if (!whole && row == 0) A.rec[cta * 2 + D.slot] = {D.cf, D.parts, D.q0, D.n, D.kvh};
+      };
+      auto inverse = [&](float L) { return whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f; };
+      if (solo) {
+        // One chunk: its group ends it while the other is at the next segment.
+        // (The second half's l goes where the first half left its maximum, which
+        // only the second half has read, and only the first writes again.)
+        float& l1 = T.top[(st0 >> 1) & 1][g][0][row];
+        if (half == 1) l1 = l;
+        if (!(ok = exchange())) break;
+        if (half == 0) {
+          const float L = l + l1, f = inverse(L);
+          if (has) ok = wait(&T.o_done[g], (uint32_t)(st0 >> 1) & 1u);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 16) {
+            uint32_t o[16];
+            float v[16];
+            if (has) tc_ld16(t_o + c, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = has ? __uint_as_float(o[i]) * f : 0.f;
+            put(c, v);
+          }
+          tc_fence_before();
+          put_sums(m, L);
+        }
+        done(seg);
+        continue;
+      }
       // The second half's l joins the first's, and the groups hand theirs
       // over; then the two groups' first warps add both groups' sums, the
       // one's 64 dims and the other's.
@@ -599,7 +681,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
         if (row == 0) T.has[g] = has;
         __syncwarp();
         if (lane == 0) mbar_arrive(&T.ml_full);
-        ok = wait(&T.ml_full, (uint32_t)seg & 1u);
+        ok = wait(&T.ml_full, (uint32_t)shared & 1u);
         const bool has0 = ok && T.has[0], has1 = ok && T.has[1];
         if (ok && has0) ok = wait(&T.o_done[0], (uint32_t)(n0 - 1) & 1u);
         if (ok && has1) ok = wait(&T.o_done[1], (uint32_t)(n1 - 1) & 1u);
@@ -607,45 +689,30 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
         tc_fence_after();
         const float(&ml0)[2][64] = T.top[n0 & 1][0], (&ml1)[2][64] = T.top[n1 & 1][1];
         const float m0 = has0 ? ml0[0][row] : -INFINITY, m1 = has1 ? ml1[0][row] : -INFINITY, M = fmaxf(m0, m1);
-        const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - M), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
-        const float L = (has0 ? ml0[1][row] : 0.f) * f0 + (has1 ? ml1[1][row] : 0.f) * f1;
-        const bool whole = D.parts == 1;
-        const size_t prow = (size_t)(cta * 2 + D.slot) * rows + row;
-        const float f = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
+        const float e0 = m0 == -INFINITY ? 0.f : ex2(m0 - M), e1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
+        const float L = (has0 ? ml0[1][row] : 0.f) * e0 + (has1 ? ml1[1][row] : 0.f) * e1;
+        const float f = inverse(L);
 #pragma unroll 1
-        for (int c = 64 * g; c < 64 * g + 64; c += 32) {
-          uint32_t o0[32], o1[32];
-          float v[32];
-          if (has0) tc_ld32(tmem + t_lane + kTcO + c, o0);
-          if (has1) tc_ld32(tmem + t_lane + kTcO + 128 + c, o1);
+        for (int c = 64 * g; c < 64 * g + 64; c += 16) {
+          uint32_t o0[16], o1[16];
+          float v[16];
+          if (has0) tc_ld16(tmem + t_lane + kTcO + c, o0);
+          if (has1) tc_ld16(tmem + t_lane + kTcO + 128 + c, o1);
           tc_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            v[i] = has0 ? __uint_as_float(o0[i]) * f0 : 0.f;
-            if (has1) v[i] += __uint_as_float(o1[i]) * f1;
+          for (int i = 0; i < 16; ++i) {
+            v[i] = has0 ? __uint_as_float(o0[i]) * e0 : 0.f;
+            if (has1) v[i] += __uint_as_float(o1[i]) * e1;
+            v[i] *= f;
           }
-          if (live && whole) {
-            uint4* out = reinterpret_cast<uint4*>(a.o + (D.q0 + r) * a.os + h * 128 + c);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              out[i] = make_uint4(pa_pack(v[8 * i] * f, v[8 * i + 1] * f), pa_pack(v[8 * i + 2] * f, v[8 * i + 3] * f),
-                                  pa_pack(v[8 * i + 4] * f, v[8 * i + 5] * f), pa_pack(v[8 * i + 6] * f, v[8 * i + 7] * f));
-          } else if (live) {
-            float4* out = reinterpret_cast<float4*>(A.part_o + prow * 128 + c);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) __stcg(out + i, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
-          }
+          put(c, v);
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&T.epi_done);
-        if (g == 0) {
-          if (live && whole && a.lse)
-            a.lse[(size_t)(D.q0 + r) * a.nq + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-          if (live && !whole) __stcg(reinterpret_cast<float2*>(A.part_ml + 2 * prow), make_float2(M, L));
-          if (!whole && row == 0) A.rec[cta * 2 + D.slot] = {D.cf, D.parts, D.q0, D.n, D.kvh};
-        }
+        if (g == 0) put_sums(M, L);
       }
+      ++shared;
       done(seg);
     }
     if (!ok) *abort = 1;
