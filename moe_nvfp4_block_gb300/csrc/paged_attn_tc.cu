@@ -369,14 +369,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
       if (D.count == 0) break;
       // the segment's rows wait in registers until the last one's are done with
       const int nrow = D.n * a.group, c = lane & 15, i0 = lane >> 4;
+      // (every second row: a head of the group, at least three, and the next
+      // verify row after the last; with a division for each the one warp took
+      // 4 us a segment)
       uint4 v[32];
+      const int r0 = i0 / a.group;
+      int head = i0 - r0 * a.group;
+      const uint16_t* src = a.q + (D.q0 + r0) * a.qs + (D.kvh * a.group + head) * 128 + 8 * c;
 #pragma unroll
       for (int u = 0; u < 32; ++u) {
-        const int i = i0 + 2 * u;
-        v[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (i < nrow) {
-          const int r = i / a.group, h = D.kvh * a.group + i - r * a.group;
-          v[u] = *reinterpret_cast<const uint4*>(a.q + (D.q0 + r) * a.qs + h * 128 + 8 * c);
+        v[u] = i0 + 2 * u < nrow ? *reinterpret_cast<const uint4*>(src) : make_uint4(0u, 0u, 0u, 0u);
+        head += 2;
+        src += 256;
+        if (head >= a.group) {
+          head -= a.group;
+          src += a.qs - a.group * 128;
         }
       }
       done(seg);
