@@ -381,9 +381,21 @@ struct PagedAttnParams {
   uint64_t wait_ns;
 };
 bool encode_page_map(CUtensorMap* m, const uint16_t* pages, int64_t rows, int box_rows, int box_halves);
+int num_sms();
 // The form for `rows` query rows a KV head: tcgen05 (its maps' boxes are one
-// dim half) for more than 32, mma.sync (both halves) up to 32.
-inline bool paged_attention_tc(int rows) { return rows > 32; }
+// dim half) or mma.sync (both halves; up to 32 rows).  A segment costs tcgen05
+// more, a chunk less; 32 rows, 8 KV heads, by mma.sync and by tcgen05:
+//   19 sequences of 4096 positions  76 us, 57   1 of 16,384  27, 23
+//   76 of 500                       45, 46      76 of 56     16, 18
+//   32 with a window of 512         31, 38   3 of up to 200  10, 12
+// so 17 to 32 rows take it where the tables have room for at least 8 chunks an
+// SM and no window cuts the sequences short.  Up to 16 rows the bytes bound
+// mma.sync as well; from 33 on it has too few registers for their sums.
+inline bool paged_attention_tc(const PagedAttnArgs& a) {
+  const int rows = a.max_rows * a.group;
+  const long long chunks = (long long)a.p.n_seqs * a.p.nkv * (((long long)a.p.max_pages << a.p.lps) / 64 + 1);
+  return rows > 32 || (rows > 16 && (a.window == 0 || a.window >= 1024) && chunks >= 8LL * num_sms());
+}
 cudaError_t launch_paged_attention_tc(const PagedAttnParams& a, int padded_rows, cudaStream_t s);
 cudaError_t launch_paged_attention(const PagedAttnParams& a, cudaStream_t s);
 
@@ -408,8 +420,6 @@ cudaError_t launch_logits(const LogitArgs& a, cudaStream_t s);
 uint64_t wait_limit_ns();
 void rope_freqs(const moe_attn_pos& p, double* f, double* temp);
 moe_status check_pos(const moe_attn_pos* p);
-
-int num_sms();
 
 // Every kernel of the library asks for the same L1/shared-memory split (all
 // shared): an SM that runs one kernel's CTAs can then take the next kernel's

@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kPjWarps * 32) k_paged_join(const __grid_const
 
 cudaError_t launch_paged_attention(const PagedAttnParams& A, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  const int want = paged_attention_tc(A.a.max_rows * A.a.group) ? num_sms() : 2 * num_sms();
+  const int want = paged_attention_tc(A.a) ? num_sms() : 2 * num_sms();
   cfg.gridDim = dim3(want < kPagedMaxCtas ? want : kPagedMaxCtas);
   cfg.blockDim = dim3(kPaThreads);
   const int rows = A.a.max_rows * A.a.group, MT = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
@@ -564,7 +564,7 @@ cudaError_t launch_paged_attention(const PagedAttnParams& A, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   auto run = [&](auto kern, cudaError_t e) { return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, kern, A) : e; };
-  const cudaError_t e = paged_attention_tc(rows) ? launch_paged_attention_tc(A, 16 * MT, s)
+  const cudaError_t e = paged_attention_tc(A.a) ? launch_paged_attention_tc(A, 16 * MT, s)
                         : MT == 1 ? run(k_paged_attn<1>, prepare_kernel<k_paged_attn<1>>((int)smem))
                                   : run(k_paged_attn<2>, prepare_kernel<k_paged_attn<2>>((int)smem));
   if (e != cudaSuccess) return e;

@@ -1,5 +1,6 @@
-// paged_attn_tc.cu -- the paged attention for 33 to 64 query rows a KV head
-// (verify rows x heads of the KV head) on the 5th-generation tensor cores.
+// paged_attn_tc.cu -- the paged attention for up to 64 query rows a KV head
+// (verify rows x heads of the KV head) on the 5th-generation tensor cores
+// (paged_attention_tc chooses).
 //
 // Same work list, ring and join as paged_attn.cu (one CTA an SM, five 32 KB
 // stages).  With 64 rows the products are 256 multiply-adds a byte of keys
@@ -369,7 +370,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
       if (D.count == 0) break;
       // the segment's rows wait in registers until the last one's are done with
       const int nrow = D.n * a.group, c = lane & 15, i0 = lane >> 4;
-      // (every second row: a head of the group, at least three, and the next
+      // (every second row: a head of the group, at least two, and the next
       // verify row after the last; with a division for each the one warp took
       // 4 us a segment)
       uint4 v[32];

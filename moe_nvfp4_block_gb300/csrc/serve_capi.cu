@@ -201,7 +201,7 @@ moe_status moe_paged_attention(const moe_paged_kv* kv, const uint16_t* q, int64_
   A.wait_ns = wait_limit_ns();
   const int64_t rows = (int64_t)kv->n_pages * kv->nkv * kv->page_size;
   const int box = kv->page_size < 64 ? kv->page_size : 64;
-  const int halves = paged_attention_tc(max_rows * a.group) ? 1 : 2;
+  const int halves = paged_attention_tc(a) ? 1 : 2;
   if (!encode_page_map(&A.km, kv->kpages, rows, box, halves) || !encode_page_map(&A.vm, kv->vpages, rows, box, halves))
     return MOE_ERR_CUDA;
   return launch_paged_attention(A, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;

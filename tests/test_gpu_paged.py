@@ -82,6 +82,18 @@ def test_long_and_unequal_lengths(M, lens, rows):
     check(M, lens, rows, 8, 2, 64, seed=3)
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(window=2000, prefix=[0, 7, 3000]), dict(softcap=20.0, first=[4000, 1, 0])])
+@pytest.mark.parametrize("rows,nq,nkv", [([8, 5, 7], 8, 2), ([16, 11, 1], 4, 2), ([5, 6, 4], 10, 2)])
+def test_middling_rows_over_long_tables(M, rows, nq, nkv, kw):
+    # 17 to 32 query rows a KV head where the tables have room for long sequences
+    check(M, [26000, 3, 9000], rows, nq, nkv, 64, seed=8, **kw)
+
+
+def test_middling_rows_with_distance_bias(M):
+    slopes = 2.0 ** -torch.arange(1, 9, device="cuda").float()
+    check(M, [26000, 20, 300], [8, 5, 7], 8, 2, 32, seed=9, slopes=slopes)
+
+
 @pytest.mark.parametrize("kw", [
     dict(window=1), dict(window=5), dict(window=64), dict(window=200), dict(window=10**6), dict(softcap=5.0),
     dict(softcap=30.0, window=33), dict(scale=0.02), dict(window=17, prefix=[0, 3, 100, 17, 2000]),
