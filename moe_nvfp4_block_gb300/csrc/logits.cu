@@ -1,16 +1,21 @@
 // logits.cu -- the rules of a batch of rows on their logits (penalties for
 // repeated tokens, biases, grammar masks) and each row's argmax, in one pass.
 //
-// CTA (tile, row) owns `tile` consecutive tokens of a row.  The history is
-// turned into a short list of the tile's repeated tokens: a bit map of the
-// tile, the number of bits before each of its words, and, by a second look at
-// the history, the tokens' counts at their places in the list.  The penalties
-// (a division among them) are taken once per listed token.  The walk over all
-// logits (bias, mask, store, running maximum) holds listed tokens at -inf, and
-// the list's own pass behind it stores and compares them, in the list's rising
-// order, so that a warp's 32 lie near one another.  More than kLgList listed
-// tokens are worked on a stretch of the tile at a time.  The row's last CTA (a
-// ticket) takes the best of the tiles.
+// CTA (tile, row) owns `tile` consecutive tokens of a row.  Tiles of up to 4096
+// count their repeated tokens in a table with a place for each, and the walk
+// over the logits (penalty, bias, mask, store, running maximum) looks there.
+// Longer tiles turn the history into a short list: a bit map of the tile, the
+// number of bits before each of its words, and, by a second look at the
+// history, the tokens' counts at their places in the list; the penalties (a
+// division among them) are taken once per listed token, the walk holds listed
+// tokens at -inf, and the list's own pass behind it stores and compares them,
+// in the list's rising order, so that a warp's 32 lie near one another.  More
+// than kLgList listed tokens are worked on a stretch of the tile at a time.
+// The row's last CTA (a ticket) takes the best of the tiles.
+//
+// (A short tile by the list takes five more waits: 8.1 us against 6.1 for one
+// row of 151,936 with a history of 700.  A long one by the table would leave
+// its threads too little to do between two looks at the history.)
 //
 // What bounds it: the logits read and written once, and above that the
 // instructions of the walk and the looks at the history.  256 rows of 128,003
@@ -63,6 +68,7 @@ constexpr int kLgRing = 4;  // lines a thread has asked for ahead of the one it 
 template <typename T, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logits(const __grid_constant__ LogitArgs a) {
   constexpr int N = 16 / sizeof(T);  // elements of a line
+  constexpr bool DENSE = THREADS == 256;  // a count for every token of the tile, no list
   extern __shared__ __align__(16) uint4 s_ring[];  // [kLgRing][THREADS] lines of x
   unsigned* s_bits = reinterpret_cast<unsigned*>(s_ring + kLgRing * THREADS);  // [tile / 32] bit map
   __shared__ float s_bv[THREADS / 32];
@@ -70,9 +76,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logits(const __grid
   const moe_logit_rules& R = a.rules;
   const int r = blockIdx.y, V = a.V, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nw = a.tile / 32;
-  int* s_pre = reinterpret_cast<int*>(s_bits + nw);               // [nw] bits before the word
-  int* s_cnt = s_pre + nw;                                        // [kLgList] counts, then values
-  int* s_tok = s_cnt + kLgList;                                   // [kLgList] elements of the tile
+  int* s_pre = reinterpret_cast<int*>(s_bits + nw);                          // [nw] bits before the word
+  int* s_cnt = DENSE ? reinterpret_cast<int*>(s_bits) : s_pre + nw;          // [kLgList] counts, then values
+  int* s_tok = s_cnt + kLgList;                                              // [kLgList] elements of the tile
   pdl_wait();
   pdl_launch_dependents();
   const T* x = static_cast<const T*>(a.x) + r * a.xs;
@@ -110,7 +116,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logits(const __grid
   const float rep = R.tokens && R.repetition ? R.repetition[r] : 1.f;
   const float pres = R.tokens && R.presence ? R.presence[r] : 0.f;
   const float freq = R.tokens && R.frequency ? R.frequency[r] : 0.f;
-  int h0 = 0, h1 = 0, n = 0;  // the history; listed tokens of the tile
+  int h0 = 0, h1 = 0, n = 0;  // the history; listed tokens of the tile (DENSE: whether it has any)
   // f(e) for every token of the history that is element e of the tile
   auto history = [&](auto f) {
     auto one = [&](int v) {
@@ -133,7 +139,14 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logits(const __grid
   if (R.tokens) {
     h0 = max(0, R.begin[r]);
     h1 = min(R.n_tokens, R.end[r]);
-    if (h0 < h1) {
+    if (DENSE && h0 < h1) {
+      for (int i = tid; i < a.tile / 4; i += THREADS) reinterpret_cast<uint4*>(s_cnt)[i] = make_uint4(0u, 0u, 0u, 0u);
+      __syncthreads();
+      history([&](int e) { atomicAdd(&s_cnt[e], 1); });
+      __syncthreads();
+      n = 1;
+    }
+    if (!DENSE && h0 < h1) {
       for (int i = tid; i < nw / 4; i += THREADS) reinterpret_cast<uint4*>(s_bits)[i] = make_uint4(0u, 0u, 0u, 0u);
       __syncthreads();
       history([&](int e) { atomicOr(&s_bits[e >> 5], 1u << (e & 31)); });
@@ -163,6 +176,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logits(const __grid
       __syncthreads();
     }
   }
+  auto penalise = [&](float f, int c) {
+    f = f > 0.f ? __fdiv_rn(f, rep) : __fmul_rn(f, rep);
+    return __fsub_rn(f, __fadd_rn(pres, __fmul_rn((float)c, freq)));
+  };
+
   float bv = -INFINITY;
   int bi = -1, k = 0;
   float wmax = -INFINITY;  // of the warp's lanes' bv
@@ -197,7 +215,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logits(const __grid
       const int v0 = EDGE ? max(v, 0) : v, v1 = EDGE ? min(v + N, V) - 1 : v + N - 1;
       bits = __funnelshift_r(__ldg(allow + (v0 >> 5)), __ldg(allow + (v1 >> 5)), v0 & 31) << (v0 - v) & in;
     }
-    if (n > 0 && in) bits &= ~(s_bits[e0 >> 5] >> (e0 & 31));
+    if (!DENSE && n > 0 && in) bits &= ~(s_bits[e0 >> 5] >> (e0 & 31));
     cp_async_wait<kLgRing - 1>();
     const uint4 line = s_ring[k % kLgRing * THREADS + tid];
     fetch(k + kLgRing);
@@ -209,6 +227,20 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logits(const __grid
     float f[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) f[i] = load(e[i]);
+    if (DENSE && n > 0) {
+      int c[N];
+#pragma unroll
+      for (int i = 0; i < N; i += 4) {
+        const int4 q = *reinterpret_cast<const int4*>(s_cnt + e0 + i);
+        c[i] = q.x;
+        c[i + 1] = q.y;
+        c[i + 2] = q.z;
+        c[i + 3] = q.w;
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (c[i] > 0) f[i] = penalise(f[i], c[i]);
+    }
     if (wide) {
       switch (bias_mis) {
         case 0: lg_add<N, 0>(b, f); break;
@@ -256,8 +288,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logits(const __grid
   // stretches [w_lo, w_hi) of the bit map's words with at most kLgList listed tokens
   for (int w_lo = 0, w_hi; w_lo < nw; w_lo = w_hi) {
     w_hi = nw;
-    const int p0 = n > 0 ? s_pre[w_lo] : 0;
-    if (n > 0) {
+    const int p0 = !DENSE && n > 0 ? s_pre[w_lo] : 0;
+    if (!DENSE && n > 0) {
       int m = n - p0;
       if (m > kLgList) {  // as many of a warp's lines (N words) as fit
         int lo = w_lo / N + 1, hi = nw / N - 1;
@@ -287,9 +319,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logits(const __grid
         for (int u = 0; u < 4; ++u) {
           const int i = i0 + u * THREADS;
           if (i >= m) break;
-          float f = load(xl[u]);
-          f = f > 0.f ? __fdiv_rn(f, rep) : __fmul_rn(f, rep);
-          s_cnt[i] = __float_as_int(__fsub_rn(f, __fadd_rn(pres, __fmul_rn((float)s_cnt[i], freq))));
+          s_cnt[i] = __float_as_int(penalise(load(xl[u]), s_cnt[i]));
         }
       }
       __syncthreads();
@@ -303,7 +333,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logits(const __grid
     }
     __syncthreads();
     // the stretch's listed tokens
-    if (n > 0) {
+    if (!DENSE && n > 0) {
       const int m = (w_hi < nw ? s_pre[w_hi] : n) - p0;
       for (int i = tid; i < m; i += THREADS) {
         const int e = s_tok[i], v = e + j0 - phase;
@@ -378,14 +408,19 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logits(const __grid
   }
 }
 
-// Tokens of a CTA: 1024 times a power of two up to kLogitTile, the one with
-// the least waves x (tile + what a CTA costs besides, about 4096 tokens' time).
+// Tokens of a CTA, a multiple of 1024: a row in n parts, the n with the least
+// waves x (tile + what a CTA costs besides, about 4096 tokens' time).  (146
+// rows of 157,142: parts of 79,872 and no second wave take 28 us, 131,072 and
+// the rest 50.)
 static int logit_tile(int R, int V) {
-  int best = 1024;
+  const int slots = 2 * num_sms();
+  const auto part = [&](int n) { return ((V + 7 + n - 1) / n + 1023) / 1024 * 1024; };
+  const int n0 = (V + 7 + kLogitTile - 1) / kLogitTile, n1 = 4 * slots / R < (V + 7) / 1024 + 1 ? 4 * slots / R : (V + 7) / 1024 + 1;
+  int best = part(n0);
   long long cost = -1;
-  for (int t = 1024; t <= kLogitTile; t *= 2) {
-    const long long ctas = (long long)R * ((V + t - 1) / t);
-    const long long waves = (ctas + 2LL * num_sms() - 1) / (2LL * num_sms());
+  for (int n = n0; n <= n1 || n == n0; ++n) {
+    const int t = part(n);
+    const long long waves = ((long long)R * ((V + 7 + t - 1) / t) + slots - 1) / slots;
     const long long c = waves * ((t < V ? t : V) + 4096);
     if (cost < 0 || c < cost) {
       cost = c;
@@ -401,7 +436,7 @@ cudaError_t launch_logits(const LogitArgs& a0, cudaStream_t s) {
   a.ntile = (a.V + 7 + a.tile - 1) / a.tile;  // the phase shifts a row by up to 7 elements
   const bool wide = a.tile > 4096;
   const auto ring = [](int threads) { return 16 * kLgRing * threads; };
-  const auto list = [](int tile) { return tile / 4 + 8 * kLgList; };
+  const auto list = [](int tile) { return tile > 4096 ? tile / 4 + 8 * kLgList : 4 * tile; };
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.ntile, a.R);
   cfg.blockDim = dim3(wide ? 512 : 256);
