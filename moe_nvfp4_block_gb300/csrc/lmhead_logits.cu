@@ -13,7 +13,7 @@
 //    pair of rows, with the weight in both halves; x, its rows' bf16 side by
 //    side in a word, is unpacked once for eight rows (four rows and half as
 //    many registers, twelve warps: 262 us; rows apart: 233);
-//  * eight warps hold the sums of 16 rows, twelve those of 8 or 4 (K 8: 144 us with
+//  * eight warps hold the sums of 16 or 12 rows, twelve those of 8 or 4 (K 8: 144 us with
 //    eight; ten, uneven over the four schedulers, 151; an earlier form);
 //  * slots of 512 columns (of 256: 287 us), counted without divisions (221 and
 //    235 us, an earlier form);
@@ -223,11 +223,14 @@ static cudaError_t launch_lmhead_logits_t(const LmHeadArgs& a, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, k_lmhead_logits<KR>, a);
 }
 
-// Rows are padded to 4, 8 or 16.  Up to 4 the weights' bytes bound it, and K 1
+// Rows are padded to 4, 8, 12 (172 us where 16 take 207) or 16.  Up to 4 the weights' bytes bound it, and K 1
 // takes what K 4 takes: 97 and 100 us at H 2048, V 151,936 (92 at the copy's
 // bandwidth), 15 at H 1024, V 32,003 (10).
 cudaError_t launch_lmhead_logits(const LmHeadArgs& a, cudaStream_t s) {
-  return a.K <= 4 ? launch_lmhead_logits_t<4>(a, s) : a.K <= 8 ? launch_lmhead_logits_t<8>(a, s) : launch_lmhead_logits_t<16>(a, s);
+  return a.K <= 4   ? launch_lmhead_logits_t<4>(a, s)
+         : a.K <= 8  ? launch_lmhead_logits_t<8>(a, s)
+         : a.K <= 12 ? launch_lmhead_logits_t<12>(a, s)
+                     : launch_lmhead_logits_t<16>(a, s);
 }
 
 }  // namespace moe

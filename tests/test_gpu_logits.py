@@ -284,6 +284,22 @@ def test_lm_head_logits(M, K, H, V):
     assert torch.equal(first.int(), tok)
 
 
+@pytest.mark.parametrize("K", [2, 5, 7, 9, 12, 13])
+def test_lm_head_logits_of_any_row_count(M, K):
+    # the bits are a row's own, whatever rows are beside it
+    g = torch.Generator(device="cuda").manual_seed(K)
+    x = torch.randn(16, 768, generator=g, device="cuda").bfloat16()
+    W = torch.randn(1303, 768, generator=g, device="cuda").bfloat16()
+    ws = torch.zeros(M.lib.moe_lm_head_workspace_size(16), dtype=torch.uint8, device="cuda")
+    all_, some = torch.empty(16, 1303, device="cuda"), torch.empty(K, 1303, device="cuda")
+    M.moe_lm_head_logits(x, W, all_, ws)
+    M.moe_lm_head_logits(x[:K], W, some, ws)
+    assert torch.equal(some, all_[:K])
+    want = x.double() @ W.double().T
+    bound = 768 * 2.0 ** -24 * (x.double().abs() @ W.double().abs().T)  # a rounding a term
+    assert bool(((all_.double() - want).abs() <= bound).all())
+
+
 def test_lm_head_logits_wait_limit(M):
     K, H, V = 4, 2048, 4096
     x = torch.randn(K, H, device="cuda").bfloat16()
