@@ -475,29 +475,26 @@ def moe_lm_head_argmax(x_norm, W, tok, ws, best_logit=None, stream=None):
 
 def moe_lm_head_logits(x_norm, W, logits, ws, stream=None):
     """logits float32 [K, V]: every logit moe_lm_head_argmax chooses from."""
-    (K, H), dev = x_norm.shape, x_norm.device
-    _like(x_norm, torch.bfloat16, (K, H), "x_norm")
-    _like(W, torch.bfloat16, (W.shape[0], H), "W", dev)
-    _like(logits, torch.float32, (K, W.shape[0]), "logits", dev)
-    _workspace(ws, dev)
-    _check(lib.moe_lm_head_logits(_ptr(x_norm), x_norm.shape[0], x_norm.shape[1], _ptr(W), W.shape[0], _ptr(logits),
-                                  _ptr(ws), ws.numel(), _stream(stream)), "moe_lm_head_logits")
+    (K, H), dev, index, V = x_norm.shape, x_norm.device, x_norm.get_device(), W.shape[0]
+    _call("moe_lm_head_logits", index, stream, lib.moe_lm_head_logits,
+          _like(x_norm, torch.bfloat16, (K, H), "x_norm"), K, H, _like(W, torch.bfloat16, (V, H), "W", dev), V,
+          _like(logits, torch.float32, (K, V), "logits", dev), *_workspace(ws, index))
 
 
 def _like(t, dtype, shape, what, device=None):
     """Refuses a tensor the library would misread: it sees an address only."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
     if device is not None and t.device != device:
         raise ValueError(f"{what} is on {t.device}, not {device}")
     return t.data_ptr()
 
 
-def _workspace(ws, device):
-    if ws.get_device() != device.index or not ws.is_contiguous():
-        raise ValueError(f"the workspace must be a contiguous tensor on {device}")
+def _workspace(ws, index):
+    if ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError(f"the workspace must be a contiguous tensor on the call's device ({index})")
     return ws.data_ptr(), ws.numel()
 
 
@@ -568,25 +565,29 @@ def _starts(kv, row_start):
     return row_start.data_ptr()
 
 
-def _call(what, device, stream, f, *args):
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _call(what, index, stream, f, *args):
     """f(*args, stream) on the tensors' device, on its current stream if none is given."""
-    i = device.index
-    if device.type != "cuda":
-        raise ValueError(f"{what} works on CUDA tensors, not on {device}")
-    s = torch._C._cuda_getCurrentRawStream(i) if stream is None else stream.cuda_stream
-    if torch._C._cuda_getDevice() == i:
+    if index < 0:
+        raise ValueError(f"{what} works on CUDA tensors")
+    s = _raw_stream(index) if stream is None else stream.cuda_stream
+    if _current_device() == index:
         status = f(*args, s)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             status = f(*args, s)
     if status:
         raise MoeError(status, what)
 
 
 def _heads(t, what):
-    if t.shape[-1] % 128:
+    n, odd = divmod(t.shape[-1], 128)
+    if odd:
         raise ValueError(f"{what} must have heads * 128 columns")
-    return t.shape[-1] // 128
+    return n
 
 
 def moe_paged_kv_append(kv: PagedKV, k_new, v_new, row_start, ws, q=None, q_out=None, pos: moe_attn_pos | None = None,
@@ -604,8 +605,8 @@ def moe_paged_kv_append(kv: PagedKV, k_new, v_new, row_start, ws, q=None, q_out=
         nq = _heads(q, "q")
         qp, qs = _strided(q, "q", kv, T, nq * 128)
         op, os_ = _strided(q_out, "q_out", kv, T, nq * 128)
-    _call("moe_paged_kv_append", kv.device, stream, lib.moe_paged_kv_append, kv._ref, qp, qs, kp, ks, vp, vs, T, nq,
-          _starts(kv, row_start), None if pos is None else ctypes.byref(pos), op, os_, *_workspace(ws, kv.device))
+    _call("moe_paged_kv_append", kv.index, stream, lib.moe_paged_kv_append, kv._ref, qp, qs, kp, ks, vp, vs, T, nq,
+          _starts(kv, row_start), None if pos is None else ctypes.byref(pos), op, os_, *_workspace(ws, kv.index))
 
 
 def moe_paged_attention(kv: PagedKV, q, row_start, o, ws, max_rows, scores: PagedScores | None = None, lse=None,
@@ -622,8 +623,8 @@ def moe_paged_attention(kv: PagedKV, q, row_start, o, ws, max_rows, scores: Page
                 raise ValueError(f"{what} must have {n} values on {kv.device}")
         ref = scores._ref
     lp = _like(lse, torch.float32, (T, nq), "lse", kv.device)
-    _call("moe_paged_attention", kv.device, stream, lib.moe_paged_attention, kv._ref, qp, qs, T, max_rows, nq,
-          _starts(kv, row_start), ref, op, os_, lp, *_workspace(ws, kv.device))
+    _call("moe_paged_attention", kv.index, stream, lib.moe_paged_attention, kv._ref, qp, qs, T, max_rows, nq,
+          _starts(kv, row_start), ref, op, os_, lp, *_workspace(ws, kv.index))
 
 
 class LogitRules:
@@ -672,13 +673,16 @@ def logits_workspace(R: int, V: int, device="cuda") -> torch.Tensor:
 def moe_logits_constrain(logits, rules: LogitRules | None, ws, out=None, tok=None, best=None, stream=None):
     """Applies ``rules`` to ``logits`` (float32 or bf16 [R, V], rows may be
     strided) and takes each row's argmax; ``out`` may be ``logits``."""
-    R, V = logits.shape
+    (R, V), stride, dtype, index = logits.shape, logits.stride(), logits.dtype, logits.get_device()
     dev = logits.device
-    if logits.dtype not in (torch.float32, torch.bfloat16) or logits.stride(1) != 1 or not logits.is_cuda:
+    if (dtype is not torch.float32 and dtype is not torch.bfloat16) or stride[1] != 1 or index < 0:
         raise ValueError("logits must be a float32 or bf16 CUDA tensor [R, V] with unit column stride")
-    if out is not None and (out.shape != logits.shape or out.dtype != logits.dtype or out.stride(1) != 1 or
-                            out.device != dev):
-        raise ValueError("out must be like logits")
+    op = os_ = 0
+    if out is not None:
+        ostride = out.stride()
+        if out.shape != (R, V) or out.dtype is not dtype or ostride[1] != 1 or out.get_device() != index:
+            raise ValueError("out must be like logits")
+        op, os_ = out.data_ptr(), ostride[0]
     ref = None
     if rules is not None:
         b, a = rules.tensors["bias"], rules.tensors["allow"]
@@ -686,11 +690,10 @@ def moe_logits_constrain(logits, rules: LogitRules | None, ws, out=None, tok=Non
                 (a is not None and a.shape[-1] != (V + 31) // 32)):
             raise ValueError(f"the rules are not for {R} rows of {V} logits on {dev}")
         ref = rules._ref
-    _call("moe_logits_constrain", dev, stream, lib.moe_logits_constrain, logits.data_ptr(),
-          MOE_LOGITS_BF16 if logits.dtype == torch.bfloat16 else MOE_LOGITS_F32, logits.stride(0), R, V, ref,
-          None if out is None else out.data_ptr(), 0 if out is None else out.stride(0),
+    _call("moe_logits_constrain", index, stream, lib.moe_logits_constrain, logits.data_ptr(),
+          MOE_LOGITS_BF16 if dtype is torch.bfloat16 else MOE_LOGITS_F32, stride[0], R, V, ref, op, os_,
           _like(tok, torch.int32, (R,), "tok", dev), _like(best, torch.float32, (R,), "best", dev),
-          *_workspace(ws, dev))
+          *_workspace(ws, index))
 
 
 def moe_workspace_error(ws, stream=None) -> int:

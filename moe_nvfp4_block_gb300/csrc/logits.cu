@@ -415,10 +415,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_logits(const __grid
 static int logit_tile(int R, int V) {
   const int slots = 2 * num_sms();
   const auto part = [&](int n) { return ((V + 7 + n - 1) / n + 1023) / 1024 * 1024; };
-  const int n0 = (V + 7 + kLogitTile - 1) / kLogitTile, n1 = 4 * slots / R < (V + 7) / 1024 + 1 ? 4 * slots / R : (V + 7) / 1024 + 1;
-  int best = part(n0);
+  const int least = (V + 7 + kLogitTile - 1) / kLogitTile, most = (V + 7) / 1024 + 1;
+  int best = part(least);
   long long cost = -1;
-  for (int n = n0; n <= n1 || n == n0; ++n) {
+  for (int w = 0; w <= 4; ++w) {  // the shortest parts of each number of waves
+    int n = w * slots / R;
+    n = n < least ? least : n > most ? most : n;
     const int t = part(n);
     const long long waves = ((long long)R * ((V + 7 + t - 1) / t) + slots - 1) / slots;
     const long long c = waves * ((t < V ? t : V) + 4096);
