@@ -14,15 +14,23 @@
 // same queries again, so that the scores also lie in the tensor memory lanes
 // that the other two of an SM's four warp slots reach: thread (row, half)
 // owns 32 scores of a row, and maximum and sum need one exchange with one
-// other thread.  (Two sequences of 65,003 and 131,001 positions, 64 rows, 8 KV
-// heads: 136 us, 5.9 TB/s; by mma.sync 349.)  For O, rows 64-127 read whatever follows P and end where nobody
-// looks.
+// other thread.  For O, rows 64-127 read whatever follows P and end where
+// nobody looks.  (Two sequences of 65,003 and 131,001 positions, 64 rows, 8 KV
+// heads: 134 us, 6.0 TB/s; by mma.sync 349.  152 units of 4096: 58 us, 64 with
+// capped scores, 67 with a bias by distance, where the keys and values alone
+// take 47 at a copy's bandwidth.)
 //
 // Two groups of four such warps take even and odd chunks, each with its own
 // S, P and O (so one group's softmax runs beside the other's products) and
 // its own running maximum m; O is only rescaled when the maximum grows by more
 // than 2^8 (p <= 256 then; the result is the same, sums and outputs being in
-// FP32).  At a segment's end the first group adds the two.
+// FP32).  At a segment's end the first warps of both groups add the two groups'
+// sums; a segment of one chunk is its group's alone, and the other goes on with
+// the next.  Such short segments take about 3 us each, what one thread row does
+// from its scores to its output, two at a time; outputs staged through shared
+// memory to be stored in whole lines took no less.  All 168 registers a thread
+// are in use: 32 columns of tensor memory at a time at a segment's end instead
+// of 16 spill, and 134 us become 139.
 //
 // Hidden positions: as in paged_attn.cu a slice with hidden positions is
 // looked over for infinite or NaN values, and such a slice is kept out of the
