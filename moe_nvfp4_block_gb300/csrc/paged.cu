@@ -12,7 +12,7 @@
 // double-precision reduction (rd / 2 a row, shared by the row's heads) is the
 // only arithmetic that counts, so a CTA takes whole rows.  8061 rows of 64
 // heads with 64 rotary dims: 56 us, 4.8 TB/s read and written; 5967 rows of 10
-// heads with 128: 21 us where the bytes take 5, the angles' doubles the rest.
+// heads with 128: 16 us where the bytes take 5, the angles' doubles the rest.
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -68,7 +68,8 @@ __device__ __forceinline__ uint32_t& word(uint4& v, int i) { return reinterpret_
 
 }  // namespace
 
-// CTA j: rows [rows j, rows (j + 1)).  The CTA copies the row starts, finds
+// CTA j: rows [rows j, rows (j + 1)): one, or as many as leave one wave, up to 4
+// (1696 rows of 18 heads: 7.6 us where a CTA a row takes 9.9).  The CTA copies the row starts, finds
 // its rows' sequences and slots, takes the angles' sines and cosines (thread
 // per pair), then walks its rows' heads.
 // VEC (rd / 2 a multiple of 8): eight lanes a head, each with two 16-byte
@@ -78,7 +79,9 @@ __device__ __forceinline__ uint32_t& word(uint4& v, int i) { return reinterpret_
 // pieces on.  Two heads a lane are in flight, the first two from before
 // anything else is known.  The arithmetic is 3 instructions an element (one
 // piece a lane, its partner by shuffles, one float at a time: 12, which bound
-// the kernel: 74 us against 56 for 8061 rows of 64 heads).
+// the kernel: 74 us against 56 for 8061 rows of 64 heads).  With 16 heads or
+// fewer a CTA works on two or four rows side by side (5967 rows of 10: 16 us
+// against 21 for one after another).
 // Else: 16 lanes a head, each element's partner loaded.
 template <bool VEC>
 __global__ void __launch_bounds__(kApThreads) k_paged_append(const __grid_constant__ PagedAppendArgs a) {
@@ -91,8 +94,9 @@ __global__ void __launch_bounds__(kApThreads) k_paged_append(const __grid_consta
   const int t0 = blockIdx.x * a.rows, ps = 1 << P.lps;
   const int nqu = a.q ? a.nq : 0, units = nqu + 2 * P.nkv, half = a.rd >> 1;
   // VEC: this lane's pieces of a head, and whether they turn
-  constexpr int HS = kApThreads / (VEC ? 8 : 16);  // heads side by side
-  const int hl = half >> 3, l8 = threadIdx.x & 7, h0 = threadIdx.x / (VEC ? 8 : 16);
+  constexpr int HS = kApThreads / (VEC ? 8 : 16);  // heads side by side: G of a row, HS / G rows
+  const int G = !VEC || units > 16 ? HS : units > 8 ? 16 : 8;
+  const int hl = half >> 3, l8 = threadIdx.x & 7, hs = threadIdx.x / (VEC ? 8 : 16), h0 = hs & (G - 1), r0 = hs / G;
   const bool turns = VEC && l8 < hl;
   const int d0 = 8 * (turns ? l8 : 2 * l8), d1 = turns ? d0 + half : d0 + 8;
   auto source = [&](int t, int u) {
@@ -103,7 +107,7 @@ __global__ void __launch_bounds__(kApThreads) k_paged_append(const __grid_consta
   auto load = [&](int t, int u0) {
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      const int u = u0 + k * HS + h0;
+      const int u = u0 + k * G + h0;
       if (t >= P.T || u >= units) continue;
       const uint16_t* src = source(t, u);
       x[k] = *reinterpret_cast<const uint4*>(src + d0);
@@ -112,7 +116,7 @@ __global__ void __launch_bounds__(kApThreads) k_paged_append(const __grid_consta
   };
   pdl_wait();
   pdl_launch_dependents();
-  if (VEC) load(t0, 0);
+  if (VEC && r0 < a.rows) load(t0 + r0, 0);
   for (int i = threadIdx.x; i <= P.n_seqs; i += kApThreads) s_start[i] = P.start[i];
   __syncthreads();
   if (threadIdx.x < a.rows) {
@@ -145,7 +149,7 @@ __global__ void __launch_bounds__(kApThreads) k_paged_append(const __grid_consta
     if (s_pos[r] >= 0) rope_cs(s_pos[r], a.freq[j], s_cos[r][j], s_sin[r][j]);
   }
   __syncthreads();
-  for (int r = 0; r < a.rows; ++r) {
+  for (int r = r0; r < a.rows; r += HS / G) {
     const int t = t0 + r;
     if (s_pos[r] < 0) continue;  // no sequence's row
     const long long slot = s_slot[r];
@@ -166,11 +170,11 @@ __global__ void __launch_bounds__(kApThreads) k_paged_append(const __grid_consta
           n2[i] = make_f2(-s.x, -s.y);
         }
       }
-      for (int u0 = 0; u0 < units; u0 += U * HS) {
-        if (r > 0 || u0 > 0) load(t, u0);
+      for (int u0 = 0; u0 < units; u0 += U * G) {
+        if (r > r0 || u0 > 0) load(t, u0);
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-          const int u = u0 + k * HS + h0;
+          const int u = u0 + k * G + h0;
           if (u >= units) continue;
           if (turns && u < nqu + P.nkv) {
 #pragma unroll
@@ -223,7 +227,8 @@ __global__ void __launch_bounds__(kApThreads) k_paged_append(const __grid_consta
 
 cudaError_t launch_paged_append(const PagedAppendArgs& a0, cudaStream_t s) {
   PagedAppendArgs a = a0;
-  a.rows = a.p.T >= kApRows * 4 * num_sms() ? kApRows : 1;
+  const int wave = 4 * num_sms();
+  a.rows = a.p.T >= kApRows * wave ? kApRows : (a.p.T + wave - 1) / wave;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((a.p.T + a.rows - 1) / a.rows);
   cfg.blockDim = dim3(kApThreads);

@@ -423,6 +423,13 @@ def test_append_many_rows(M, rows):
     append_case(M, [(i * 37) % 90 for i in range(len(rows))], rows, 2, 1, 32, rd=128)
 
 
+@pytest.mark.parametrize("rows", [[610], [1500, 301, 3], [2400, 500]])
+@pytest.mark.parametrize("nq,nkv", [(8, 1), (4, 2), (2, 2), (16, 2)])
+def test_append_rows_side_by_side(M, nq, nkv, rows):
+    # few heads and many rows: a CTA works on several rows at once
+    append_case(M, [3] * len(rows), rows, nq, nkv, 16, rd=64, in_place=nq == 8)
+
+
 def test_append_past_the_pages_is_recorded(M):
     lens, rows = [30, 10, 5], [4, 2, 3]
     k, v, table, n, start = ref.make_cache(lens, rows, 1, 16, 0, spare=0)
