@@ -69,7 +69,7 @@ __device__ __forceinline__ uint32_t& word(uint4& v, int i) { return reinterpret_
 }  // namespace
 
 // CTA j: rows [rows j, rows (j + 1)): one, or as many as leave one wave, up to 4
-// (1696 rows of 18 heads: 7.6 us where a CTA a row takes 9.9).  The CTA copies the row starts, finds
+// (1696 rows of 20 heads: 7.6 us where a CTA a row takes 9.9).  The CTA copies the row starts, finds
 // its rows' sequences and slots, takes the angles' sines and cosines (thread
 // per pair), then walks its rows' heads.
 // VEC (rd / 2 a multiple of 8): eight lanes a head, each with two 16-byte
