@@ -109,6 +109,9 @@ struct PaSegment {
   __device__ __forceinline__ int pos(int j) const { return (j < s.np ? s.cp + j : s.cm + j - s.np) * kPaChunk; }
 };
 
+// (Out of line: what runs before the first load should be short.)
+__device__ __noinline__ long long pa_div(long long x, long long y) { return x / y; }
+
 // The producer warp: the CTA's share of the call's slots (plan: every
 // sequence), chunk by chunk into the ring.
 //   out.begin(segment, stage): a segment begins with this stage (false: gave up)
@@ -142,7 +145,7 @@ __device__ __forceinline__ int pa_produce(const PagedAttnParams& A, PaRing<STAGE
   const int G = (int)min((long long)gridDim.x, W);
   const bool small = W < 1 << 22;  // 32-bit divisions do
   auto div = [&](long long x, long long y) {
-    return small ? (long long)((unsigned)x / (unsigned)y) : x / y;
+    return small ? (long long)((unsigned)x / (unsigned)y) : pa_div(x, y);
   };
   const long long w0 = cta < G ? div(cta * W, G) : W, w1 = cta < G ? div((cta + 1) * W, G) : W;
   long long base = inc - sum;
