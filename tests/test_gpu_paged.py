@@ -535,3 +535,23 @@ def test_wait_limit_is_recorded_and_recovered(M, nq, rows):
     o, lse, _ = run(M, k, v, table, n, start, q, nq, 8, ws=ws)
     assert M.moe_workspace_error(ws) == 0
     ref.check_attention(o, lse, ref.attention(q, k, v, table, lens, rows, nq))
+
+
+def test_wait_limit_with_many_rows(M):
+    # the same for more than 32 query rows a KV head
+    lens, rows, nq = [3000, 500], [9, 12], 8
+    k, v, table, n, start = ref.make_cache(lens, rows, 2, 64, 0)
+    q = queries(sum(rows), nq, 1)
+    ws = M.paged_workspace(M.PagedKV(k, v, table, n), 16, nq)
+    torch.cuda.synchronize()
+    try:
+        M.moe_debug_set_wait_limit_ns(0)
+        run(M, k, v, table, n, start, q, nq, 16, ws=ws)
+        torch.cuda.synchronize()
+    finally:
+        M.moe_debug_set_wait_limit_ns(2_000_000_000)
+    assert M.moe_workspace_error(ws) == M.MOE_ERR_DEVICE_TIMEOUT
+    ws.zero_()
+    o, lse, _ = run(M, k, v, table, n, start, q, nq, 16, ws=ws)
+    assert M.moe_workspace_error(ws) == 0
+    ref.check_attention(o, lse, ref.attention(q, k, v, table, lens, rows, nq))
