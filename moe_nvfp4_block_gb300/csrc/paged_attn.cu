@@ -51,6 +51,9 @@ namespace {
 constexpr int kPaWarps = 8;                      // compute warps
 constexpr int kPaThreads = (kPaWarps + 1) * 32;  // and the producer
 constexpr int kPaStages = 3;
+// Slots before a unit's chunks (two: 29.7 us against 28.9 for 17 documents with a
+// bias by distance, 32.1 against 30.8 for 32 sequences with a window of 512).
+constexpr int kPaUnit = 1;
 
 // A chunk as its stage's readers see it.
 struct PaDesc {
@@ -169,7 +172,7 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
         return true;
       }
     };
-    const int st = pa_produce(A, T.ring, plan, cta, lane, Out{A, T, smem, policy_evict_first(), lane, br, a.window});
+    const int st = pa_produce<kPaUnit>(A, T.ring, plan, cta, lane, Out{A, T, smem, policy_evict_first(), lane, br, a.window});
     __syncthreads();  // every warp is done with the ring
     if (*abort && lane == 0) pa_drain(T.ring, st, P.err);
     return;

@@ -12,7 +12,6 @@ namespace {
 constexpr int kPaChunk = 64;                     // positions of a chunk
 constexpr int kPaHalf = kPaChunk * 256;          // a stage's keys (or values)
 constexpr int kPaStageBytes = 2 * kPaHalf;
-constexpr int kPaUnit = 1;                       // slots before a unit's chunks
 constexpr uint64_t kPaDrainNs = 2000000000ull;
 
 template <int STAGES>
@@ -113,14 +112,14 @@ struct PaSegment {
 __device__ __noinline__ long long pa_div(long long x, long long y) { return x / y; }
 
 // The producer warp: the CTA's share of the call's slots (plan: every
-// sequence), chunk by chunk into the ring.
+// sequence; UNIT of them before each unit's chunks), chunk by chunk into the ring.
 //   out.begin(segment, stage): a segment begins with this stage (false: gave up)
 //   out.stage(segment, j, stage, bytes): one lane, before the loads of chunk j
 //   out.put(slot, box, row, barrier): loads a box's keys and values, the
 //     cache rows from `row` on
 //   out.end(stage): the CTA's work is written down
 // Returns the number of stages begun; *abort is set where a wait ran out.
-template <int STAGES, class Out>
+template <int UNIT, int STAGES, class Out>
 __device__ __forceinline__ int pa_produce(const PagedAttnParams& A, PaRing<STAGES>& T, const PaSeq* plan, int cta, int lane,
                                           Out out) {
   const PagedAttnArgs& a = A.a;
@@ -129,7 +128,7 @@ __device__ __forceinline__ int pa_produce(const PagedAttnParams& A, PaRing<STAGE
   const int lbr = min(P.lps, 6), br = 1 << lbr;  // positions of a box
   // lane l sums the sequences [l k, (l + 1) k); the lane that holds the
   // CTA's first slot finds its sequence
-  auto slots = [&](int nch) { return nch > 0 ? (long long)P.nkv * (nch + kPaUnit) : 0LL; };
+  auto slots = [&](int nch) { return nch > 0 ? (long long)P.nkv * (nch + UNIT) : 0LL; };
   const int k = (P.n_seqs + 31) / 32;
   long long sum = 0;
   for (int i = 0; i < k; ++i)
@@ -175,13 +174,13 @@ __device__ __forceinline__ int pa_produce(const PagedAttnParams& A, PaRing<STAGE
     return ok;
   };
   bool live = true;
-  int kvh = s.nch > 0 ? (int)div(w0 - base, s.nch + kPaUnit) : 0;
+  int kvh = s.nch > 0 ? (int)div(w0 - base, s.nch + UNIT) : 0;
   // page cache: lane l holds box l & (boxes - 1) of chunk cj + (l >> lnb) of sequence cb
   int cb = -1, cj = 0, crow = 0;
   bool cload = false;
   while (live) {
-    const int span = s.nch + kPaUnit;
-    const long long rs = base + (long long)kvh * span + kPaUnit, re = rs + s.nch;  // the unit's chunks
+    const int span = s.nch + UNIT;
+    const long long rs = base + (long long)kvh * span + UNIT, re = rs + s.nch;  // the unit's chunks
     if (rs >= w1 || w0 >= w1) break;
     PaSegment g{s, kvh, rs >= w0 ? 0 : (int)(w0 - rs), (int)(min(re, w1) - rs), 0, 1, rs >= w0};
     if (rs < w0 || re > w1) {

@@ -16,7 +16,7 @@
 // owns 32 scores of a row, and maximum and sum need one exchange with one
 // other thread.  For O, rows 64-127 read whatever follows P and end where
 // nobody looks.  (Two sequences of 65,003 and 131,001 positions, 64 rows, 8 KV
-// heads: 134 us, 6.0 TB/s; by mma.sync 349.  152 units of 4096: 58 us, 64 with
+// heads: 132 us, 6.1 TB/s; by mma.sync 349.  152 units of 4096: 58 us, 64 with
 // capped scores, 67 with a bias by distance, where the keys and values alone
 // take 47 at a copy's bandwidth.)
 //
@@ -30,7 +30,7 @@
 // from its scores to its output, two at a time; outputs staged through shared
 // memory to be stored in whole lines took no less.  All 168 registers a thread
 // are in use: 32 columns of tensor memory at a time at a segment's end instead
-// of 16 spill, and 134 us become 139.
+// of 16 spill, and 133 us become 139.
 //
 // Hidden positions: as in paged_attn.cu a slice with hidden positions is
 // looked over for infinite or NaN values, and such a slice is kept out of the
@@ -42,6 +42,9 @@ namespace moe {
 namespace {
 
 constexpr int kTcStages = 5;
+// Slots before a unit's chunks: what its ends cost in chunks (236 units of 1 to
+// 5911 positions: 42 us, 48 with one slot, 43 with six).
+constexpr int kTcUnit = 4;
 constexpr int kTcThreads = 384;
 constexpr int kTcP = 2 * 8192;   // a group's P: hi, lo [64 rows][64 positions] bf16
 constexpr int kTcQ = 2 * 16384;  // Q: [dim half][64 rows twice][64 dims] bf16
@@ -284,7 +287,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
         return false;
       }
     };
-    issued = pa_produce(A, T.ring, plan, cta, lane,
+    issued = pa_produce<kTcUnit>(A, T.ring, plan, cta, lane,
                         Out{A, T, ring, abort, policy_evict_first(), lane, 1 << min(P.lps, 6), 0});
   } else if (warp == kTcMma || warp == kTcMmaO) {
     // ---------------------------------------------------------------- products
