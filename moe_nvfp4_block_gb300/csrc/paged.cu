@@ -34,12 +34,6 @@ __device__ __forceinline__ int seq_of(const int* start, int n, int t) {
   return lo - 1 < n ? lo - 1 : -1;
 }
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-
 // Two floats, and two correctly rounded operations at a time.
 typedef unsigned long long f2;
 __device__ __forceinline__ f2 make_f2(float x, float y) {
@@ -51,7 +45,7 @@ __device__ __forceinline__ f2 unpack2(uint32_t w) { return make_f2(__uint_as_flo
 __device__ __forceinline__ uint32_t pack2(f2 p) {
   float x, y;
   asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
-  return pack2(x, y);
+  return pack_bf16(x, y);
 }
 __device__ __forceinline__ f2 mul2(f2 a, f2 b) {
   f2 d;
@@ -216,7 +210,7 @@ __global__ void __launch_bounds__(kApThreads) k_paged_append(const __grid_consta
               z[i] = d < half ? __fsub_rn(xc, ys) : __fadd_rn(xc, ys);
             }
           }
-          w = make_uint4(pack2(z[0], z[1]), pack2(z[2], z[3]), pack2(z[4], z[5]), pack2(z[6], z[7]));
+          w = make_uint4(pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3]), pack_bf16(z[4], z[5]), pack_bf16(z[6], z[7]));
         }
         uint16_t* dst = live ? target(u) : nullptr;
         if (dst) *reinterpret_cast<uint4*>(dst + e0) = w;

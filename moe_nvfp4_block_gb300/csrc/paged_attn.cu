@@ -341,8 +341,8 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
         for (int nb = 0; nb < MT; ++nb) {
           const float x = ex2(sc[nb][2 * hr] - ref), y = ex2(sc[nb][2 * hr + 1] - ref);
           l[hr] += x + y;
-          const uint32_t hi = pa_pack(x, y);
-          const uint32_t lo = pa_pack(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u));
+          const uint32_t hi = pack_bf16(x, y);
+          const uint32_t lo = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u));
           const uint32_t at = p_hi + (g + 8 * hr) * 128 + (((MT * part + nb) ^ g) << 4) + 4 * t;
           asm volatile("st.shared.u32 [%0], %1;\n st.shared.u32 [%0 + 2048], %2;" ::"r"(at), "r"(hi), "r"(lo) : "memory");
         }
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
           const float inv = L == 0.f ? 0.f : 1.f / L;
           uint32_t* out = reinterpret_cast<uint32_t*>(a.o + (D.q0 + r) * a.os + h * 128 + 16 * MT * part);
 #pragma unroll
-          for (int nb = 0; nb < 2 * MT; ++nb) out[4 * nb + t] = pa_pack(o[nb][2 * hr] * inv, o[nb][2 * hr + 1] * inv);
+          for (int nb = 0; nb < 2 * MT; ++nb) out[4 * nb + t] = pack_bf16(o[nb][2 * hr] * inv, o[nb][2 * hr + 1] * inv);
           if (a.lse && t == 0 && part == 0)
             a.lse[(size_t)(D.q0 + r) * a.nq + h] = L == 0.f ? -INFINITY : (m[hr] + log2f(L)) * 0.6931471805599453f;
         } else {
@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(kPjWarps * 32) k_paged_join(const __grid_const
     const int r = i / a.group, h = R.kvh * a.group + i - r * a.group;
     const float inv = L == 0.f ? 0.f : 1.f / L;
     *reinterpret_cast<uint2*>(a.o + (R.q0 + r) * a.os + h * 128 + 4 * lane) =
-        make_uint2(pa_pack(v.x * inv, v.y * inv), pa_pack(v.z * inv, v.w * inv));
+        make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
     if (a.lse && lane == 0)
       a.lse[(size_t)(R.q0 + r) * a.nq + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
   };

@@ -73,11 +73,6 @@ __device__ __forceinline__ bool pa_all(int len, int n, int first, int prefix, in
   return p0 >= first && p1 <= len && (window == 0 || p0 > len + n - 1 - window || p1 < prefix);
 }
 
-__device__ __forceinline__ uint32_t pa_pack(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
 // 2^x to 2 ulp, 0 below 2^-126.
 __device__ __forceinline__ float ex2(float x) {
   float y;

@@ -578,8 +578,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             const float x = s[8 * c + 2 * u], y = s[8 * c + 2 * u + 1];
-            hi[u] = pa_pack(x, y);
-            lo[u] = pa_pack(x - __uint_as_float(hi[u] << 16), y - __uint_as_float(hi[u] & 0xFFFF0000u));
+            hi[u] = pack_bf16(x, y);
+            lo[u] = pack_bf16(x - __uint_as_float(hi[u] << 16), y - __uint_as_float(hi[u] & 0xFFFF0000u));
           }
           const uint32_t at = p_row + (((4 * half + c) ^ (row & 7)) << 4);
           asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3])
@@ -643,8 +643,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
           uint4* out = reinterpret_cast<uint4*>(a.o + (D.q0 + r) * a.os + h * 128 + c);
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            out[i] = make_uint4(pa_pack(v[8 * i], v[8 * i + 1]), pa_pack(v[8 * i + 2], v[8 * i + 3]),
-                                pa_pack(v[8 * i + 4], v[8 * i + 5]), pa_pack(v[8 * i + 6], v[8 * i + 7]));
+            out[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                                pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
         } else if (live) {
           float4* out = reinterpret_cast<float4*>(A.part_o + prow * 128 + c);
 #pragma unroll
