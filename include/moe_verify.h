@@ -492,8 +492,9 @@ size_t moe_paged_workspace_size(int max_rows, int nq, int nkv);
  * rounding at the end.  (YaRN's temperature, which the attention block puts
  * into its scale, (0.1 ln yarn_factor + 1)^2 / sqrt(128), is the caller's to
  * put into moe_paged_scores.)
- * A row whose position has no page (MOE_ERR_CAPACITY) or a page id out of
- * range is not stored; its query is turned all the same.
+ * A row whose position has no page (MOE_ERR_CAPACITY), a page id out of range
+ * or a sequence of negative length is not stored; its query is turned all the
+ * same.  Nothing is written for a sequence with wrong rows (see above).
  */
 moe_status moe_paged_kv_append(const moe_paged_kv* kv, const uint16_t* q, int64_t q_stride, const uint16_t* k_new,
                                int64_t k_stride, const uint16_t* v_new, int64_t v_stride, int n_rows, int nq,

@@ -23,8 +23,17 @@ namespace {
 constexpr int kApThreads = 256;
 constexpr int kApRows = 4;  // most rows of a CTA
 
-// Row t's sequence: the last b with start[b] <= t, or -1.
-__device__ __forceinline__ int seq_of(const int* start, int n, int t) {
+// A sequence's rows [s0, s1) that are none of a call's T rows (no rows: anywhere).
+__device__ __forceinline__ bool wrong_rows(int s0, int s1, int T) { return s0 != s1 && (s0 < 0 || s1 < s0 || s1 > T); }
+
+// Row t's sequence: the last b with start[b] <= t, or -1.  With `wrong` rows
+// somewhere the starts need not rise: the last right sequence that has t.
+__device__ __forceinline__ int seq_of(const int* start, int n, int t, int T, bool wrong) {
+  if (wrong) {
+    for (int b = n - 1; b >= 0; --b)
+      if (!wrong_rows(start[b], start[b + 1], T) && start[b] <= t && t < start[b + 1]) return b;
+    return -1;
+  }
   int lo = 0, hi = n + 1;  // start[lo - 1] <= t < start[hi]
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -111,11 +120,17 @@ __global__ void __launch_bounds__(kApThreads) k_paged_append(const __grid_consta
   pdl_wait();
   pdl_launch_dependents();
   if (VEC && r0 < a.rows) load(t0 + r0, 0);
-  for (int i = threadIdx.x; i <= P.n_seqs; i += kApThreads) s_start[i] = P.start[i];
-  __syncthreads();
+  bool wrong = false;
+  for (int i = threadIdx.x; i <= P.n_seqs; i += kApThreads) {
+    const int s0 = P.start[i], s1 = P.start[min(i + 1, P.n_seqs)];
+    s_start[i] = s0;
+    wrong |= wrong_rows(s0, s1, P.T);
+  }
+  wrong = __syncthreads_or(wrong);
+  if (wrong && blockIdx.x == 0 && threadIdx.x == 0) atomicCAS(P.err, 0, (int)MOE_ERR_INVALID_ARG);
   if (threadIdx.x < a.rows) {
     const int t = t0 + threadIdx.x;
-    const int b = t < P.T ? seq_of(s_start, P.n_seqs, t) : -1;
+    const int b = t < P.T ? seq_of(s_start, P.n_seqs, t, P.T, wrong) : -1;
     long long slot = -1;
     int pos = -1;
     if (b >= 0) {

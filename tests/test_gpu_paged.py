@@ -448,6 +448,67 @@ def test_append_past_the_pages_is_recorded(M):
     assert torch.equal(k, was_k)
 
 
+WRONG_STARTS = [[-1, 2, 4, 6], [0, 2, 4, 7], [0, 4, 2, 6], [0, 2, -1, 6], [0, 2, 4, 2**31 - 1], [0, 2, -2**31, 6],
+                [-2**31, 0, 3, 6], [-2**31, 2**31 - 1, -5, 6], [7, 9, 4, 6], [6, 4, 2, 0], [100, 100, 0, 3]]
+
+
+@pytest.mark.parametrize("rd", [0, 20, 64])
+@pytest.mark.parametrize("start", WRONG_STARTS)
+def test_append_skips_wrong_rows_and_records_them(M, start, rd):
+    # as in the attention: a sequence whose rows are not the call's is left out, the others are not
+    lens, T, nq = [30, 10, 5], 6, 2
+    k, v, table, n, good = ref.make_cache([40] * 3, [4] * 3, 1, 16, 0)
+    n.copy_(ints(lens))
+    good = good // 2  # two rows each
+    was_k, was_v = k.clone(), v.clone()
+    kv, pos = M.PagedKV(k, v, table, n), M.attn_pos(rotary_dim=rd)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q, kn, vn = (torch.randn(T, h * HD, generator=g, device="cuda").bfloat16() for h in (nq, 1, 1))
+    out, ws = torch.full_like(q, 7.0), M.paged_workspace(kv, 1, nq)
+    M.moe_paged_kv_append(kv, kn, vn, ints(start), ws, q=q, q_out=out, pos=pos)
+    assert M.moe_workspace_error(ws) == M.MOE_ERR_INVALID_ARG
+    assert M.moe_workspace_error(ws) == 0
+    freq = ref.rotary_freqs(rd, 10000.0)
+    for t in range(T):
+        b = max([b for b in range(3) if 0 <= start[b] <= t < start[b + 1] <= T], default=None)
+        if b is None:
+            assert bool((out[t] == 7).all())
+            continue
+        p = lens[b] + t - start[b]
+        page, at = table[b, p // 16].long(), ints([p])
+        want = [ref.rotate(x[t:t + 1].double().unflatten(1, (-1, HD)), at, freq)[0] for x in (q, kn)]
+        for got, w in ((out[t].view(nq, HD), want[0]), (k[page, :, p % 16], want[1])):
+            assert bool(((got.double() - w).abs() <= 2.0 ** -8 * w.abs() + 2.0 ** -20 * 16).all())
+        assert torch.equal(v[page, 0, p % 16], vn[t])
+        k[page, :, p % 16], v[page, :, p % 16] = was_k[page, :, p % 16], was_v[page, :, p % 16]
+    assert torch.equal(k, was_k) and torch.equal(v, was_v)
+    M.moe_paged_kv_append(kv, kn, vn, good, ws, q=q, q_out=out, pos=pos)  # the workspace stays usable
+    assert M.moe_workspace_error(ws) == 0
+    assert torch.equal(v[table[2, 0].long(), 0, 5:7], vn[4:])
+
+
+def test_append_of_many_sequences_with_wrong_rows(M):
+    # several rows a CTA; two of 1000 sequences wrong, and sequences without rows
+    B, lens = 1000, [(i * 7) % 20 for i in range(1000)]
+    rows = [i % 6 for i in range(B)]
+    k, v, table, n, start = ref.make_cache(lens, rows, 1, 16, 0)
+    s = start.tolist()
+    bad = list(s)
+    bad[500] = s[500] - 3 - 2**20       # sequence 499 falls, 500 starts before the rows
+    T = s[-1] - 2                       # and the last one ends behind them
+    vn = torch.randn(T, HD, device="cuda").bfloat16()
+    kv, was = M.PagedKV(k, v, table, n), v.clone()
+    ws = M.paged_workspace(kv, 1, 1)
+    M.moe_paged_kv_append(kv, vn, vn, ints(bad), ws)
+    assert M.moe_workspace_error(ws) == M.MOE_ERR_INVALID_ARG
+    for b in range(B):
+        if b not in (499, 500, B - 1):
+            for i in range(rows[b]):
+                p = lens[b] + i
+                was[table[b, p // 16].long(), 0, p % 16] = vn[s[b] + i]
+    assert torch.equal(v, was)
+
+
 # ---------------------------------------------------------------- together
 
 def test_a_verify_loop_over_pages(M):
