@@ -67,7 +67,7 @@ __device__ __forceinline__ PaSeq pa_seq(const PagedAttnArgs& a, int b, int* err)
 // Whether some row sees a position of [p0, p1]; whether every row sees all.
 __device__ __forceinline__ bool pa_any(int len, int n, int first, int prefix, int window, int p0, int p1) {
   const int hi = len + n, lo = window > 0 ? max(first, len - window + 1) : first;
-  return (p0 < hi && p1 >= lo) || (max(p0, first) < prefix && p1 >= first);
+  return (max(p0, lo) < hi && p1 >= lo) || (max(p0, first) < prefix && p1 >= first);  // (lo may be hi: nothing visible)
 }
 __device__ __forceinline__ bool pa_all(int len, int n, int first, int prefix, int window, int p0, int p1) {
   return p0 >= first && p1 <= len && (window == 0 || p0 > len + n - 1 - window || p1 < prefix);

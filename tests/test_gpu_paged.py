@@ -115,6 +115,22 @@ def test_rows_that_see_nothing(M):
     check(M, [10, 40, 5, 300], [3, 2, 4, 1], 8, 2, 16, first=[11, 1000, 7, 2**31 - 1])
 
 
+FORMS = [([4, 3], 8, 2), ([8, 5], 8, 2), ([16, 11], 8, 2)]  # up to 16, 32 and 64 query rows a KV head
+
+
+@pytest.mark.parametrize("rows,nq,nkv", FORMS)
+@pytest.mark.parametrize("kw", [dict(), dict(window=30), dict(window=7, prefix=[9, 200])])
+def test_rows_that_see_nothing_need_no_pages(M, rows, nq, nkv, kw):
+    lens = [10, 40]
+    k, v, table, n, start = ref.make_cache(lens, rows, nkv, 16, 1)
+    table.fill_(-1)
+    q, dev = queries(sum(rows), nq, 2), {x: ints(y) if x == "prefix" else y for x, y in kw.items()}
+    for first in ([1000, 2**31 - 1], [lens[0] + rows[0], lens[1] + rows[1]]):
+        o, lse, ws = run(M, k, v, table, n, start, q, nq, max(rows), first=ints(first), **dev)
+        assert M.moe_workspace_error(ws) == 0
+        assert bool((o == 0).all()) and bool((lse == -math.inf).all())
+
+
 def test_strided_rows(M):
     check(M, [33, 129], [4, 3], 8, 2, 64, strided=True)
 
