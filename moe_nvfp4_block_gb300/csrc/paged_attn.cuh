@@ -35,7 +35,7 @@ __device__ __forceinline__ PaSeq pa_seq(const PagedAttnArgs& a, int b, int* err)
   const int q1 = P.start[b + 1];
   s.len = P.kv_len[b];
   s.first = a.first ? max(0, a.first[b]) : 0;
-  s.prefix = a.prefix && a.window > 0 ? a.prefix[b] : 0;
+  s.prefix = a.prefix && a.window > 0 ? max(0, a.prefix[b]) : 0;
   if (q1 == s.q0) return s;
   int e = 0;
   if (s.q0 < 0 || q1 < s.q0 || q1 > P.T || q1 - s.q0 > a.max_rows || s.len < 0) e = MOE_ERR_INVALID_ARG;

@@ -131,6 +131,20 @@ def test_rows_that_see_nothing_need_no_pages(M, rows, nq, nkv, kw):
         assert bool((o == 0).all()) and bool((lse == -math.inf).all())
 
 
+@pytest.mark.parametrize("rows,nq,nkv", FORMS)
+def test_limits_at_the_ends_of_their_type(M, rows, nq, nkv):
+    # below zero: as zero; past the rows: as far as there are positions
+    lens, low, high = [200, 90], -2**31, 2**31 - 1
+    k, v, table, n, start = ref.make_cache(lens, rows, nkv, 16, 1, fill=float("nan"))
+    q = queries(sum(rows), nq, 2)
+    for window, prefix, first, wp, wf in ((20, [low, low + 3], [low, -1], [0, 0], [0, 0]),
+                                          (20, [high, -1], [70, low], [10**6, 0], [70, 0]),
+                                          (high, [high, low], [0, 1], [0, 0], [0, 1])):
+        o, lse, ws = run(M, k, v, table, n, start, q, nq, max(rows), window=window, prefix=ints(prefix), first=ints(first))
+        assert M.moe_workspace_error(ws) == 0
+        ref.check_attention(o, lse, ref.attention(q, k, v, table, lens, rows, nq, window=window, prefix=wp, first=wf))
+
+
 def test_strided_rows(M):
     check(M, [33, 129], [4, 3], 8, 2, 64, strided=True)
 
