@@ -35,7 +35,7 @@
 // latency of its instructions, and with the positions split all the way (each
 // warp its own maximum and all 128 dims, four warps of 168 registers) a chunk
 // took 1.9 us and a unit's end 2.5 to 4.5.  P is split into two bf16 parts (P
-// = hi + lo to 2^-17: one bf16 P would add as much error as the output's own
+// = hi + lo to 2^-16: one bf16 P would add as much error as the output's own
 // rounding; the second product is free while the loads bound the kernel).
 //
 // Hidden positions: a score is replaced by -inf, and as 0 * v is not 0 for
@@ -341,8 +341,8 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
         for (int nb = 0; nb < MT; ++nb) {
           const float x = ex2(sc[nb][2 * hr] - ref), y = ex2(sc[nb][2 * hr + 1] - ref);
           l[hr] += x + y;
-          const uint32_t hi = pack_bf16(x, y);
-          const uint32_t lo = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u));
+          uint32_t hi, lo;
+          pa_split(x, y, hi, lo);
           const uint32_t at = p_hi + (g + 8 * hr) * 128 + (((MT * part + nb) ^ g) << 4) + 4 * t;
           asm volatile("st.shared.u32 [%0], %1;\n st.shared.u32 [%0 + 2048], %2;" ::"r"(at), "r"(hi), "r"(lo) : "memory");
         }
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
         const float L = sum[hr];
         if (D.np == 1) {
           const int r = i / a.group, h = D.kvh * a.group + i - r * a.group;
-          const float inv = L == 0.f ? 0.f : 1.f / L;
+          const float inv = pa_inverse(L);
           uint32_t* out = reinterpret_cast<uint32_t*>(a.o + (D.q0 + r) * a.os + h * 128 + 16 * MT * part);
 #pragma unroll
           for (int nb = 0; nb < 2 * MT; ++nb) out[4 * nb + t] = pack_bf16(o[nb][2 * hr] * inv, o[nb][2 * hr + 1] * inv);
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kPjWarps * 32) k_paged_join(const __grid_const
   auto part = [&](int u, int i) { return (size_t)((R.cf + u) * 2 + (u == 0)) * rows + i; };
   auto put = [&](int i, float M, float L, float4 v) {
     const int r = i / a.group, h = R.kvh * a.group + i - r * a.group;
-    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const float inv = pa_inverse(L);
     *reinterpret_cast<uint2*>(a.o + (R.q0 + r) * a.os + h * 128 + 4 * lane) =
         make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
     if (a.lse && lane == 0)

@@ -576,11 +576,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
         for (int c = 0; c < 4; ++c) {
           uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float x = s[8 * c + 2 * u], y = s[8 * c + 2 * u + 1];
-            hi[u] = pack_bf16(x, y);
-            lo[u] = pack_bf16(x - __uint_as_float(hi[u] << 16), y - __uint_as_float(hi[u] & 0xFFFF0000u));
-          }
+          for (int u = 0; u < 4; ++u) pa_split(s[8 * c + 2 * u], s[8 * c + 2 * u + 1], hi[u], lo[u]);
           const uint32_t at = p_row + (((4 * half + c) ^ (row & 7)) << 4);
           asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3])
                        : "memory");
@@ -657,7 +653,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
         if (live && !whole) __stcg(reinterpret_cast<float2*>(A.part_ml + 2 * prow), make_float2(M, L));
         if (!whole && row == 0) A.rec[cta * 2 + D.slot] = {D.cf, D.parts, D.q0, D.n, D.kvh};
       };
-      auto inverse = [&](float L) { return whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f; };
+      auto inverse = [&](float L) { return whole ? pa_inverse(L) : 1.f; };
       if (solo) {
         // One chunk: its group ends it while the other is at the next segment.
         // (The second half's l goes where the first half left its maximum, which

@@ -154,6 +154,36 @@ def test_hidden_slots_hold_anything(M, fill):
     check(M, [17, 90, 64], [2, 5, 1], 4, 2, 32, fill=fill, window=30)
 
 
+@pytest.mark.parametrize("rows,nq,nkv", FORMS)
+@pytest.mark.parametrize("equal", [False, True])
+@pytest.mark.parametrize("kw", [dict(), dict(window=170, prefix=[50, 60]), dict(first=[19, 20])])
+@pytest.mark.parametrize("lens", [[200, 90], [20000, 90], [0, 17]])
+def test_visible_infinite_values_are_what_the_formula_gives(M, rows, nq, nkv, equal, kw, lens):
+    # infinite, opposite and NaN values, seen by every row or by some; with equal scores the weights are exact in bf16
+    inf = math.inf
+    k, v, table, n, start = ref.make_cache(lens, rows, nkv, 16, 1, fill=float("nan"))
+    if equal:
+        k.zero_()
+    for b in range(2):
+        def put(p, dim, x):
+            if p < lens[b] + rows[b]:
+                v[table[b, p // 16].long(), :, p % 16, dim] = x
+        for p, dim, x in ((20, 3, inf), (40, 4, -inf), (20, 5, inf), (70, 5, -inf), (33, 6, math.nan), (3, 10, inf),
+                          (lens[b], 11, -inf), (lens[b] + 2, 12, inf), (lens[b] - 100, 13, inf)):
+            put(max(p, 0), dim, x)
+        for p in range(16, 32):
+            put(p, 8, inf)
+            put(p, 9, -inf)
+    q, dev = queries(sum(rows), nq, 2), {x: ints(y) if x != "window" else y for x, y in kw.items()}
+    o, lse, _ = run(M, k, v, table, n, start, q, nq, max(rows), **dev)
+    ro, rl, _ = ref.attention(q, k, v, table, lens, rows, nq, **kw)
+    got = o.double().reshape(ro.shape)
+    for kind in (torch.isnan, torch.isposinf, torch.isneginf):
+        assert torch.equal(kind(got), kind(ro)), kind.__name__
+    fine = torch.isfinite(ro)
+    assert bool(((got - ro)[fine].abs() <= 2.0 ** -8 * ro[fine].abs() + 2.0 ** -11 * 4).all())
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
 @pytest.mark.parametrize("window", [0, 20])
 def test_a_rows_own_bad_value_stays_its_own(M, bad, window):
