@@ -529,7 +529,7 @@ typedef struct {
  * A row that sees no position (or only scores of -inf) gives o = 0.  What
  * hidden positions hold (NaN and infinities too) changes nothing.  Infinite
  * and NaN values that a row sees give what the formula gives (a weight below
- * 2^-116 of the row's largest may count as 0, and 0 times infinity is NaN).
+ * 2^-100 of the row's largest may count as 0, and 0 times infinity is NaN).
  *   q  bf16 [n_rows][nq * 128], q_stride elements between rows (a multiple of 8)
  *   o  bf16 [n_rows][nq * 128], o_stride elements between rows (a multiple of
  *      8); may be q itself with the same stride

@@ -22,9 +22,10 @@
 //
 // Two groups of four such warps take even and odd chunks, each with its own
 // S, P and O (so one group's softmax runs beside the other's products) and
-// its own running maximum m; O is only rescaled when the maximum grows by more
-// than 2^8 (p <= 256 then; the result is the same, sums and outputs being in
-// FP32).  At a segment's end the first warps of both groups add the two groups'
+// its own running reference m; O is only rescaled when a score is above it, to
+// 8 (in log2) above that score, so that growth by less than 2^8 costs nothing
+// and no p is above 1 (with m at the maximum itself and p up to 256, p v passed
+// FP32's range for values above 1e36).  At a segment's end the first warps of both groups add the two groups'
 // sums; a segment of one chunk is its group's alone, and the other goes on with
 // the next.  Such short segments take about 3 us each, what one thread row does
 // from its scores to its output, two at a time; outputs staged through shared
@@ -50,7 +51,7 @@ constexpr int kTcP = 2 * 8192;   // a group's P: hi, lo [64 rows][64 positions] 
 constexpr int kTcQ = 2 * 16384;  // Q: [dim half][64 rows twice][64 dims] bf16
 constexpr int kTcCols = 512;     // tensor memory columns
 constexpr int kTcS = 0, kTcO = 256;  // S of chunk c at 64 (c mod 4), O of group g at 256 + 128 g
-constexpr float kTcLazy = 8.f;   // growth of the maximum (log2) that is let pass
+constexpr float kTcRoom = 8.f;   // growth of the maximum (log2) that the reference leaves room for
 // Warps: 0-3 and 4-7 softmax of the even and odd chunks (a warp reads the
 // tensor memory lanes of its number mod 4), 8 producer, 9 and 10 products (S;
 // O: one warp for both spent 870 of 2200 clocks a chunk between the two), 11
@@ -543,9 +544,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
         if (!(ok = exchange())) break;
         const float top = unit * fmaxf(mine_top, s_top[half ^ 1][row]);
         float scale = 1.f;
-        if (top > m && (m == -INFINITY || top - m > kTcLazy)) {
-          if (m != -INFINITY) scale = ex2(m - top);  // else the row's sums are zeros
-          m = top;
+        if (top > m) {
+          const float up = top + kTcRoom;
+          if (m != -INFINITY) scale = ex2(m - up);  // else the row's sums are zeros
+          m = up;
           l *= scale;
         }
         const float ref = m == -INFINITY ? 0.f : m;  // nothing visible yet

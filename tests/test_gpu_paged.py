@@ -184,6 +184,30 @@ def test_visible_infinite_values_are_what_the_formula_gives(M, rows, nq, nkv, eq
     assert bool(((got - ro)[fine].abs() <= 2.0 ** -8 * ro[fine].abs() + 2.0 ** -11 * 4).all())
 
 
+@pytest.mark.parametrize("rows,nq,nkv", FORMS)
+@pytest.mark.parametrize("seqs", [2, 200])
+@pytest.mark.parametrize("gain", [2.0, 5.0, 60.0])
+def test_weights_do_not_take_values_out_of_range(M, rows, nq, nkv, seqs, gain):
+    # a position in the middle outweighs those before by e^gain; its value times that passes FP32's
+    # range, the row's output does not
+    lens, rows = [700] * seqs, [rows[i % 2] for i in range(seqs)]
+    k, v, table, n, start = ref.make_cache(lens, rows, nkv, 64, 1)
+    k.zero_()
+    v.zero_()
+    big = min(3e38 / math.exp(gain) * 3, 1e38)
+    for b in range(seqs):
+        k[table[b, 400 // 64].long(), :, 400 % 64, 0] = 1
+        v[table[b, 400 // 64].long(), :, 400 % 64] = big
+    q = torch.zeros(sum(rows), nq * HD, device="cuda")
+    q[:, ::HD] = gain * HD ** 0.5
+    q = q.bfloat16()
+    o, lse, _ = run(M, k, v, table, n, start, q, nq, max(rows))
+    ro, rl, bound = ref.attention(q[:sum(rows[:2])], k, v, table, lens[:2], rows[:2], nq)
+    t = sum(rows[:2])
+    ref.check_attention((o[:t].double() / big), lse[:t], (ro / big, rl, bound))
+    assert bool(torch.isfinite(o).all())
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
 @pytest.mark.parametrize("window", [0, 20])
 def test_a_rows_own_bad_value_stays_its_own(M, bad, window):
