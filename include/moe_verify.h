@@ -514,7 +514,7 @@ moe_status moe_paged_kv_append(const moe_paged_kv* kv, const uint16_t* q, int64_
  */
 typedef struct {
   int window;              /* 0: none, else at least 1 */
-  float scale, softcap;    /* finite, not negative */
+  float scale, softcap;    /* 0..2^126 */
   const float* slopes;     /* [nq] or NULL */
   const int32_t* first;    /* [n_seqs] or NULL */
   const int32_t* prefix;   /* [n_seqs] or NULL */

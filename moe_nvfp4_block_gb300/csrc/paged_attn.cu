@@ -301,14 +301,15 @@ __global__ void __launch_bounds__(kPaThreads, 2) k_paged_attn(const __grid_const
 #pragma unroll
           for (int c = 0; c < 4; ++c) sc[nb][c] *= a.scale_log2;
         } else {
+          if (a.cap_log2 > 0.f) {
+            pa_capped(a, sc[nb][0], sc[nb][1]);
+            pa_capped(a, sc[nb][2], sc[nb][3]);
+          } else {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            // tanh(z) = 1 - 2 / (e^2z + 1): off by an FP32 rounding of 1, an
-            // absolute error, which is what a score needs
-            float x = sc[nb][c] * a.scale_log2;
-            if (a.cap_log2 > 0.f) x = a.cap_log2 * (1.f - 2.f * rcp(ex2(sc[nb][c] * a.cap_in) + 1.f));
-            sc[nb][c] = x + slope[c >> 1] * (float)(pb + 2 * t + (c & 1) - rp[c >> 1]);
+            for (int c = 0; c < 4; ++c) sc[nb][c] *= a.scale_log2;
           }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) sc[nb][c] += slope[c >> 1] * (float)(pb + 2 * t + (c & 1) - rp[c >> 1]);
         }
         if (!(flags >> (kPaAll + (w >> 4)) & 1)) {
           const bool some = flags >> (kPaAny + (w >> 4)) & 1;  // else its page may not even be loaded

@@ -85,6 +85,46 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
+// Two floats; two correctly rounded operations at a time.
+__device__ __forceinline__ unsigned long long pa_pair(float x, float y) {
+  unsigned long long p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+  return p;
+}
+__device__ __forceinline__ void pa_unpair(unsigned long long p, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
+}
+__device__ __forceinline__ unsigned long long pa_mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ unsigned long long pa_fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+// Two capped scores, cap tanh(x scale / cap), in the log2 domain; x, y: q . k.
+// With w = 2 log2(e) z and z the tanh's argument, 1 - 2 / (2^w + 1) is off by
+// FP32 roundings of 1 however small z is (an error of 1e-7 caps), so that below
+// |z| = 1/8 the series z (1 - z^2/3 + 2 z^4/15) takes over, its first term the
+// uncapped score: either way within 9e-7 of the score.
+__device__ __forceinline__ void pa_capped(const PagedAttnArgs& a, float& x, float& y) {
+  constexpr float h = 0.12011325348f;  // (ln 2 / 2)^2: z^2 = h w^2
+  const unsigned long long xy = pa_pair(x, y), w = pa_mul2(xy, pa_pair(a.cap_in, a.cap_in)), t = pa_mul2(w, w);
+  unsigned long long p = pa_fma2(pa_pair(2.f / 15.f * h * h, 2.f / 15.f * h * h), t, pa_pair(-h / 3.f, -h / 3.f));
+  p = pa_mul2(pa_fma2(p, t, pa_pair(1.f, 1.f)), pa_mul2(xy, pa_pair(a.scale_log2, a.scale_log2)));
+  float w0, w1, t0, t1, p0, p1;
+  pa_unpair(w, w0, w1);
+  pa_unpair(t, t0, t1);
+  pa_unpair(p, p0, p1);
+  const float l0 = __fmaf_rn(-2.f * a.cap_log2, rcp(ex2(w0) + 1.f), a.cap_log2);
+  const float l1 = __fmaf_rn(-2.f * a.cap_log2, rcp(ex2(w1) + 1.f), a.cap_log2);
+  x = t0 < 1.f / 64.f / h ? p0 : l0;
+  y = t1 < 1.f / 64.f / h ? p1 : l1;
+}
+
 // Two weights, each times kPaUp, in two bf16 parts: hi + lo to 2^-16.  Both
 // parts are positive where the weight is (hi is cut off, and kPaUp leaves more
 // than nothing for lo): an infinite value times either is then that value again,

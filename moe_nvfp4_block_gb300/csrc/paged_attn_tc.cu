@@ -484,11 +484,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_paged_attn_tc(const __grid_co
         for (int c = 0; c < 32; ++c) s[c] = __uint_as_float(sr[c]);
         if (!a.plain) {
           if (a.cap_log2 > 0.f) {
-            // tanh(z) = 1 - 2 / (e^2z + 1): off by an FP32 rounding of 1, an
-            // absolute error, which is what a score needs
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              s[c] = __fmaf_rn(-2.f * a.cap_log2, rcp(ex2(s[c] * a.cap_in) + 1.f), a.cap_log2);
+            for (int c = 0; c < 32; c += 2) pa_capped(a, s[c], s[c + 1]);
           } else {
 #pragma unroll
             for (int c = 0; c < 32; ++c) s[c] *= a.scale_log2;

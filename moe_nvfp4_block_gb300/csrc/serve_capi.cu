@@ -1,5 +1,6 @@
 // serve_capi.cu -- the C ABI of the serving operators: argument checks,
 // workspace carving and launches.
+#include <cfloat>
 #include <cmath>
 
 #include "internal.h"
@@ -170,8 +171,9 @@ moe_status moe_paged_attention(const moe_paged_kv* kv, const uint16_t* q, int64_
   if (!aligned4(lse)) return MOE_ERR_MISALIGNED;
   const moe_paged_scores none{};
   if (!scores) scores = &none;
-  if (scores->window < 0 || !(scores->scale >= 0.f) || !(scores->softcap >= 0.f) || std::isinf(scores->scale) ||
-      std::isinf(scores->softcap))
+  constexpr float most = 0x1p126f;  // times log2 e it is finite
+  if (scores->window < 0 || !(scores->scale >= 0.f && scores->scale <= most) ||
+      !(scores->softcap >= 0.f && scores->softcap <= most))
     return MOE_ERR_INVALID_ARG;
   if (!aligned4(scores->slopes) || !aligned4(scores->first) || !aligned4(scores->prefix)) return MOE_ERR_MISALIGNED;
   const PagedLayout L = paged_layout(max_rows * (nq / kv->nkv));
@@ -188,7 +190,9 @@ moe_status moe_paged_attention(const moe_paged_kv* kv, const uint16_t* q, int64_
   a.window = scores->window;
   const double log2e = 1.4426950408889634, scale = scores->scale > 0.f ? scores->scale : 1.0 / std::sqrt(128.0);
   a.scale_log2 = (float)(scale * log2e);
-  a.cap_in = scores->softcap > 0.f ? (float)(2.0 * log2e * scale / scores->softcap) : 0.f;
+  a.cap_in = 0.f;
+  if (scores->softcap > 0.f)  // as far as FP32 goes (not 0 or infinite: 0 times infinity)
+    a.cap_in = (float)std::fmin(std::fmax(2.0 * log2e * scale / scores->softcap, FLT_MIN), FLT_MAX);
   a.cap_log2 = (float)(scores->softcap * log2e);
   a.plain = !(scores->softcap > 0.f) && !scores->slopes;
   a.slopes = scores->slopes;

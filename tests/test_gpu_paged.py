@@ -103,6 +103,38 @@ def test_score_forms(M, kw, rows, nq, nkv):
     check(M, [3, 77, 200, 64, 1100], rows, nq, nkv, 32, seed=5, **kw)
 
 
+FORMS = [([4, 3], 8, 2), ([8, 5], 8, 2), ([16, 11], 8, 2)]  # up to 16, 32 and 64 query rows a KV head
+
+
+@pytest.mark.parametrize("rows,nq,nkv", FORMS)
+@pytest.mark.parametrize("cap", [1e-30, 1e-3, 1.0, 9.0, 100.0, 1e3, 1e4, 1e6, 1e9, 1e20, 2.0 ** 126])
+def test_softcaps_of_any_size(M, cap, rows, nq, nkv):
+    # the cap's error is to the score, not to the cap: the room is that of the uncapped scores
+    # (|d tanh| <= |d z|, and tanh's own 6e-7 of the score is below the 2^-20 of it there)
+    lens = [200, 90]
+    k, v, table, n, start = ref.make_cache(lens, rows, nkv, 16, 1, fill=float("nan"))
+    q = queries(sum(rows), nq, 2)
+    o, lse, _ = run(M, k, v, table, n, start, q, nq, max(rows), softcap=cap)
+    want = ref.attention(q, k, v, table, lens, rows, nq, softcap=cap)
+    bound = ref.attention(q, k, v, table, lens, rows, nq)[2]
+    ref.check_attention(o, lse, (want[0], want[1], bound), f"softcap {cap}")
+
+
+@pytest.mark.parametrize("kw", [dict(scale=2.0 ** 120, softcap=20.0), dict(scale=2.0 ** -120, softcap=2.0 ** 60),
+                                dict(scale=2.0 ** -100, softcap=2.0 ** 100)])
+def test_softcaps_far_from_the_scale(M, kw):
+    # scores at the cap's two ends (or zero), or all but equal
+    for rows, nq, nkv in FORMS:
+        lens = [200, 90]
+        k, v, table, n, start = ref.make_cache(lens, rows, nkv, 16, 1)
+        q = queries(sum(rows), nq, 2)
+        q[0] = 0
+        o, lse, _ = run(M, k, v, table, n, start, q, nq, max(rows), **kw)
+        want = ref.attention(q, k, v, table, lens, rows, nq, **kw)
+        bound = 2.0 ** -20 * (1 + 20 + want[1].abs())  # scores of at most 20 and their sums
+        ref.check_attention(o, lse, (want[0], want[1], bound), f"{kw}")
+
+
 @pytest.mark.parametrize("rows", [[2, 1, 3], [1, 1, 1]])
 def test_distance_bias(M, rows):
     slopes = 2.0 ** -torch.arange(1, 9, device="cuda").float()
@@ -113,9 +145,6 @@ def test_distance_bias(M, rows):
 def test_rows_that_see_nothing(M):
     # first past the rows' positions: o = 0, lse = -inf; some rows of a sequence only
     check(M, [10, 40, 5, 300], [3, 2, 4, 1], 8, 2, 16, first=[11, 1000, 7, 2**31 - 1])
-
-
-FORMS = [([4, 3], 8, 2), ([8, 5], 8, 2), ([16, 11], 8, 2)]  # up to 16, 32 and 64 query rows a KV head
 
 
 @pytest.mark.parametrize("rows,nq,nkv", FORMS)

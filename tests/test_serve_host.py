@@ -98,6 +98,14 @@ def test_attention_refuses_bad_scores(M, kw, status):
     assert attention(M, sc=M.moe_paged_scores(**kw)) == status
 
 
+@pytest.mark.parametrize("what", ["scale", "softcap"])
+def test_attention_scores_may_be_large_but_not_out_of_range(M, what):
+    # no rows: nothing is enqueued for what passes
+    assert attention(M, n=0, sc=M.moe_paged_scores(**{what: 2.0 ** 126})) == OK
+    assert attention(M, n=0, sc=M.moe_paged_scores(**{what: 1e-45})) == OK
+    assert attention(M, n=0, sc=M.moe_paged_scores(**{what: 1.0001 * 2.0 ** 126})) == INVALID
+
+
 def test_no_rows_is_no_work(M):
     assert append(M, n=0) == OK and attention(M, n=0) == OK
 
