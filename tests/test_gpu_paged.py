@@ -142,6 +142,22 @@ def test_distance_bias(M, rows):
     check(M, [500, 20, 3000], rows, 8, 4, 16, seed=6, slopes=-slopes / 64, softcap=20.0, window=300)
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=20.0), dict(window=300), dict(softcap=20.0, window=70, prefix=[5, 0, 40])])
+def test_distance_bias_of_many_rows(M, kw):
+    slopes = 2.0 ** -torch.arange(1, 9, device="cuda").float()
+    check(M, [500, 20, 3000], [16, 9, 12], 8, 2, 32, seed=6, slopes=slopes, **kw)
+    check(M, [500, 20, 3000], [16, 9, 12], 8, 2, 32, seed=7, slopes=-slopes / 64, **kw)
+
+
+@pytest.mark.parametrize("group,rows", [(3, [16, 11, 5]), (5, [12, 7, 1]), (7, [9, 8, 2]), (7, [5, 6, 7]), (9, [7, 3, 4]),
+                                        (11, [5, 4, 3]), (13, [4, 3, 1]), (64, [1, 1, 1]), (21, [3, 2, 1]), (3, [10, 9, 6]),
+                                        (7, [4, 3, 1]), (5, [3, 1, 2]), (17, [1, 1, 1]), (33, [1, 1, 1])])
+def test_odd_head_groups(M, group, rows):
+    for lens in ([700, 3, 64], [26000, 100, 0]):  # short and long tables
+        check(M, lens, rows, 2 * group, 2, 32, seed=group, window=0)
+    check(M, [300, 90, 8], rows, 3 * group, 3, 16, seed=group, window=65, prefix=[3, 70, 0], softcap=25.0)
+
+
 def test_rows_that_see_nothing(M):
     # first past the rows' positions: o = 0, lse = -inf; some rows of a sequence only
     check(M, [10, 40, 5, 300], [3, 2, 4, 1], 8, 2, 16, first=[11, 1000, 7, 2**31 - 1])
@@ -256,6 +272,26 @@ def test_a_rows_own_bad_value_stays_its_own(M, bad, window):
     d = (got - ro)[fine].abs()
     assert bool((d <= 2.0 ** -8 * ro[fine].abs() + 2.0 ** -11 * 4).all())
     assert bool(torch.isfinite(lse).all())
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("window", [0, 20])
+@pytest.mark.parametrize("nq", [1, 2, 4, 8])
+def test_a_bad_value_of_some_rows_in_every_form(M, bad, window, nq):
+    # as above for 8 to 64 query rows, and inf and NaN told apart
+    lens, rows = [100], [8]
+    k, v, table, n, start = ref.make_cache(lens, rows, 1, 16, 1, fill=float("nan"))
+    for p in (102, 85) if window else (102,):
+        v[table[0, p // 16].long(), 0, p % 16, 5:9] = bad
+    q = queries(8, nq, 2)
+    o, lse, _ = run(M, k, v, table, n, start, q, nq, 8, window=window)
+    ro, rl, bound = ref.attention(q, k, v, table, lens, rows, nq, window=window)
+    got = o.double().reshape(ro.shape)
+    for kind in (torch.isnan, torch.isposinf, torch.isneginf):
+        assert torch.equal(kind(got), kind(ro))
+    fine = torch.isfinite(ro)
+    assert bool(((got - ro)[fine].abs() <= 2.0 ** -8 * ro[fine].abs() + 2.0 ** -11 * 4).all())
+    assert bool(((lse.double() - rl).abs() <= bound).all())
 
 
 def test_keys_of_infinite_score(M):
@@ -397,6 +433,22 @@ def test_output_over_the_queries(M, nq, rows):
     assert torch.equal(got, o)
 
 
+@pytest.mark.parametrize("rows,nq,nkv", FORMS)
+@pytest.mark.parametrize("more", [0, 1])
+def test_output_over_the_queries_in_every_form(M, rows, nq, nkv, more):
+    lens, most = [5000, 40], min(16, max(rows) + more)
+    k, v, table, n, start = ref.make_cache(lens, rows, nkv, 64, 0)
+    q = queries(sum(rows), nq, 1, strided=True)
+    o, lse, ws = run(M, k, v, table, n, start, q, nq, most)
+    ref.check_attention(o, lse, ref.attention(q, k, v, table, lens, rows, nq))
+    wide = torch.full((sum(rows), q.stride(0)), 3.0, dtype=torch.bfloat16, device="cuda")
+    got = wide[:, HD:(nq + 1) * HD]
+    got.copy_(q)
+    M.moe_paged_attention(M.PagedKV(k, v, table, n), got, start, got, ws, most)
+    assert torch.equal(got, o)
+    assert bool((wide[:, :HD] == 3).all()) and bool((wide[:, (nq + 1) * HD:] == 3).all())
+
+
 def test_no_rows(M):
     k, v, table, n, start = ref.make_cache([5], [0], 2, 16, 0)
     kv = M.PagedKV(k, v, table, n)
@@ -421,6 +473,64 @@ def test_two_streams_at_once(M, nq, rows):
     for i in range(2):
         k, v, table = caches[i][:3]
         ref.check_attention(os_[i], None, ref.attention(qs[i], k, v, table, lens[i], rows, nq))
+
+
+@pytest.mark.parametrize("rows,nq,nkv", FORMS)
+def test_two_streams_at_once_in_every_form(M, rows, nq, nkv):
+    lens = [[6000, 300], [100, 9000]]
+    caches = [ref.make_cache(l, rows, nkv, 64, i) for i, l in enumerate(lens)]
+    kvs, qs = [M.PagedKV(*c[:4]) for c in caches], [queries(sum(rows), nq, i) for i in range(2)]
+    ws, os_ = [M.paged_workspace(kv, max(rows), nq) for kv in kvs], [torch.empty_like(q) for q in qs]
+    streams = [torch.cuda.Stream() for _ in kvs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in range(2):
+            M.moe_paged_attention(kvs[i], qs[i], caches[i][4], os_[i], ws[i], max(rows), stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        k, v, table = caches[i][:3]
+        ref.check_attention(os_[i], None, ref.attention(qs[i], k, v, table, lens[i], rows, nq))
+
+
+@pytest.mark.parametrize("rows,nq,nkv", FORMS)
+def test_graphs_of_every_form_share_a_workspace(M, rows, nq, nkv):
+    lens = [[700, 30], [5, 4000]]
+    caches = [ref.make_cache([l + 400 for l in ls], rows, nkv, 64, i) for i, ls in enumerate(lens)]
+    kvs, qs = [M.PagedKV(*c[:4]) for c in caches], [queries(sum(rows), nq, i) for i in range(2)]
+    os_, ws = [torch.empty_like(q) for q in qs], M.paged_workspace(kvs[0], max(rows), nq)
+    call = lambda i: M.moe_paged_attention(kvs[i], qs[i], caches[i][4], os_[i], ws, max(rows))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        call(0)
+    side.synchronize()
+    graphs = []
+    for i in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            call(i)
+    for add in (0, 63, 399):
+        for i in range(2):
+            kvs[i].kv_len.copy_(ints([l + add for l in lens[i]]))
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            k, v, table = caches[i][:3]
+            ref.check_attention(os_[i], None, ref.attention(qs[i], k, v, table, [l + add for l in lens[i]], rows, nq))
+    assert M.moe_workspace_error(ws) == 0
+
+
+@pytest.mark.parametrize("rows,nq,nkv", FORMS)
+def test_idle_sequences_between_long_ones(M, rows, nq, nkv):
+    # a server's slots: most have no rows this time, some of them long histories all the same
+    lens = [3000] + [(i * 13) % 200 for i in range(500)] + [2000] + [(i * 7) % 90 for i in range(400)]
+    all_rows = [rows[0]] + [0] * 500 + [rows[1]] + [0] * 400
+    k, v, table, n, start = ref.make_cache(lens, all_rows, nkv, 64, 0)
+    n[7], n[600] = -5, 2**31 - 1  # nobody looks at the length of a sequence without rows
+    q = queries(sum(rows), nq, 1)
+    o, lse, ws = run(M, k, v, table, n, start, q, nq, max(rows))
+    assert M.moe_workspace_error(ws) == 0
+    ref.check_attention(o, lse, ref.attention(q, k, v, table, lens, all_rows, nq))
 
 
 def test_a_captured_step_appends_and_attends(M):
@@ -727,5 +837,25 @@ def test_wait_limit_with_many_rows(M):
     assert M.moe_workspace_error(ws) == M.MOE_ERR_DEVICE_TIMEOUT
     ws.zero_()
     o, lse, _ = run(M, k, v, table, n, start, q, nq, 16, ws=ws)
+    assert M.moe_workspace_error(ws) == 0
+    ref.check_attention(o, lse, ref.attention(q, k, v, table, lens, rows, nq))
+
+
+@pytest.mark.parametrize("rows,nq,nkv", FORMS)
+def test_wait_limit_in_every_form(M, rows, nq, nkv):
+    lens = [3000, 500]
+    k, v, table, n, start = ref.make_cache(lens, rows, nkv, 64, 0)
+    q = queries(sum(rows), nq, 1)
+    ws = M.paged_workspace(M.PagedKV(k, v, table, n), max(rows), nq)
+    torch.cuda.synchronize()
+    try:
+        M.moe_debug_set_wait_limit_ns(0)
+        run(M, k, v, table, n, start, q, nq, max(rows), ws=ws)
+        torch.cuda.synchronize()
+    finally:
+        M.moe_debug_set_wait_limit_ns(2_000_000_000)
+    assert M.moe_workspace_error(ws) == M.MOE_ERR_DEVICE_TIMEOUT
+    ws.zero_()
+    o, lse, _ = run(M, k, v, table, n, start, q, nq, max(rows), ws=ws)
     assert M.moe_workspace_error(ws) == 0
     ref.check_attention(o, lse, ref.attention(q, k, v, table, lens, rows, nq))
