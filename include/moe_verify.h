@@ -540,6 +540,9 @@ typedef struct {
  * A sequence with a wrong length or rows (see above) is skipped, its rows
  * left as they were; where a page id is out of range the sequence's rows are
  * undefined.
+ * The same call gives the same bits.  The order in which a row's positions are
+ * added depends on the whole call (its lengths, max_rows, max_pages), so
+ * another call may round the row otherwise.
  */
 moe_status moe_paged_attention(const moe_paged_kv* kv, const uint16_t* q, int64_t q_stride, int n_rows, int max_rows,
                                int nq, const int32_t* row_start, const moe_paged_scores* scores, uint16_t* o,
@@ -549,7 +552,7 @@ moe_status moe_paged_attention(const moe_paged_kv* kv, const uint16_t* q, int64_
  * The lm_head's logits themselves, for rules and samplers that need all of
  * them: logits[r][v] = x_norm_r . W_v, bit for bit the logits whose argmax
  * moe_lm_head_argmax takes (shapes, order and workspace as there).
- *   logits  float [K][V] out
+ *   logits  float [K][V] out, 16-byte aligned
  */
 moe_status moe_lm_head_logits(const uint16_t* x_norm, int K, int H, const uint16_t* W, int V, float* logits, void* ws,
                               size_t ws_bytes, void* stream);
@@ -591,8 +594,9 @@ size_t moe_logits_workspace_size(int R, int V);
 /*
  * Applies the rules to R rows of logits and takes each row's argmax:
  *   logits, out  float or bf16 (type MOE_LOGITS_F32 / MOE_LOGITS_BF16)
- *                [R][V], stride / out_stride elements between rows; out may
- *                be NULL, or logits itself with the same stride
+ *                [R][V], stride / out_stride elements between rows, the
+ *                first row 16-byte aligned (the others anywhere); out may be
+ *                NULL, or logits itself with the same stride
  *   tok   int32 [R] or NULL: the argmax of the FP32 values (lowest index on
  *         a tie, a NaN never); -1 where no token is above -inf
  *   best  float [R] or NULL: that FP32 value (-inf with tok -1)

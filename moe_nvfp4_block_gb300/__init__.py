@@ -672,7 +672,8 @@ def logits_workspace(R: int, V: int, device="cuda") -> torch.Tensor:
 
 def moe_logits_constrain(logits, rules: LogitRules | None, ws, out=None, tok=None, best=None, stream=None):
     """Applies ``rules`` to ``logits`` (float32 or bf16 [R, V], rows may be
-    strided) and takes each row's argmax; ``out`` may be ``logits``."""
+    strided, the first one 16-byte aligned) and takes each row's argmax; ``out``
+    may be ``logits``."""
     (R, V), stride, dtype, index = logits.shape, logits.stride(), logits.dtype, logits.get_device()
     dev = logits.device
     if (dtype is not torch.float32 and dtype is not torch.bfloat16) or stride[1] != 1 or index < 0:

@@ -389,8 +389,10 @@ int num_sms();
 //   76 of 500                       45, 46      76 of 56     16, 18
 //   32 with a window of 512         31, 38   3 of up to 200  10, 12
 // so 17 to 32 rows take it where the tables have room for at least 8 chunks an
-// SM and no window cuts the sequences short.  Up to 16 rows the bytes bound
-// mma.sync as well; from 33 on it has too few registers for their sums.
+// SM and no window cuts the sequences short.  (The lengths are on the device: a
+// table wider than its sequences need takes tcgen05 for short ones too.)  Up to
+// 16 rows the bytes bound mma.sync as well; from 33 on it has too few registers
+// for their sums.
 inline bool paged_attention_tc(const PagedAttnArgs& a) {
   const int rows = a.max_rows * a.group;
   const long long chunks = (long long)a.p.n_seqs * a.p.nkv * (((long long)a.p.max_pages << a.p.lps) / 64 + 1);

@@ -19,8 +19,8 @@
 //
 // What bounds it: the logits read and written once, and above that the
 // instructions of the walk and the looks at the history.  256 rows of 128,003
-// bf16 tokens (131 MB in all, whose plain copy takes 45 us) take 25 us without
-// rules, 39 with biases and masks, 59 with histories of 4000 as well.  So:
+// bf16 tokens (131 MB in all: 19 us at a copy's bandwidth) take 25 us without
+// rules, 39 with biases and masks, 58 with histories of 4000 as well.  So:
 //  * tiles are as long as leaves the SMs evenly filled, since every tile looks
 //    through its row's whole history: 65 us where tiles of 65,536 took 70;
 //  * lines come by cp.async, kLgRing ahead a thread, asked for before the look

@@ -12,7 +12,7 @@
 // double-precision reduction (rd / 2 a row, shared by the row's heads) is the
 // only arithmetic that counts, so a CTA takes whole rows.  8061 rows of 64
 // heads with 64 rotary dims: 56 us, 4.8 TB/s read and written; 5967 rows of 10
-// heads with 128: 16 us where the bytes take 5, the angles' doubles the rest.
+// heads with 128: 17 us where the bytes take 5, the angles' doubles the rest.
 #include "internal.h"
 #include "ptx.cuh"
 

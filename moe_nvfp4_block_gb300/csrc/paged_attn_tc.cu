@@ -16,20 +16,21 @@
 // owns 32 scores of a row, and maximum and sum need one exchange with one
 // other thread.  For O, rows 64-127 read whatever follows P and end where
 // nobody looks.  (Two sequences of 65,003 and 131,001 positions, 64 rows, 8 KV
-// heads: 132 us, 6.1 TB/s; by mma.sync 349.  152 units of 4096: 58 us, 64 with
-// capped scores, 67 with a bias by distance, where the keys and values alone
-// take 47 at a copy's bandwidth.)
+// heads: 134 us, 6 TB/s, in short runs, 136 to 143 in long ones; by mma.sync 349.
+// 152 units of 4096: 58 us, 64 with capped scores, 64 with a bias by distance,
+// 77 with both, where the keys and values alone take 47 at a copy's bandwidth.)
 //
 // Two groups of four such warps take even and odd chunks, each with its own
 // S, P and O (so one group's softmax runs beside the other's products) and
 // its own running reference m; O is only rescaled when a score is above it, to
 // 8 (in log2) above that score, so that growth by less than 2^8 costs nothing
 // and no p is above 1 (with m at the maximum itself and p up to 256, p v passed
-// FP32's range for values above 1e36).  At a segment's end the first warps of both groups add the two groups'
-// sums; a segment of one chunk is its group's alone, and the other goes on with
-// the next.  Such short segments take about 3 us each, what one thread row does
-// from its scores to its output, two at a time; outputs staged through shared
-// memory to be stored in whole lines took no less.  All 168 registers a thread
+// FP32's range for values above 1e36).  At a segment's end the first warps of
+// both groups add the two groups' sums; a segment of one chunk is its group's
+// alone, and the other goes on with the next.  Such short segments take about 3
+// us each, what one thread row does from its scores to its output, two at a
+// time; outputs staged through shared memory to be stored in whole lines took
+// no less.  All 168 registers a thread
 // are in use: 32 columns of tensor memory at a time at a segment's end instead
 // of 16 spill, and 133 us become 139.
 //
