@@ -649,9 +649,12 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_paged_attn8_tc(const __grid_c
         }
         const bool bent = !fold || !(info & kP8InfoAll);
         auto values = [&](int h) { return smem_addr(s_v) + (2 * st + h) % kT8Values * kT8V; };
-        // both halves of the chunk's values are there
+        // Both halves of the chunk's values are there.  A wait on a parity tells a phase from the one before it, not from
+        // the one before that, so the one before has to be known complete; v_full is waited for in few chunks only, but
+        // its buffers' last values are what O's last product read: that product has ended, then those were there.
         auto unpacked = [&]() {
-          return wait(&T.v_full[2 * st % kT8Values], (uint32_t)(2 * st / kT8Values) & 1u) &&
+          return (own == 0 || wait(&T.o_done[g], (uint32_t)(own - 1) & 1u)) &&
+                 wait(&T.v_full[2 * st % kT8Values], (uint32_t)(2 * st / kT8Values) & 1u) &&
                  wait(&T.v_full[(2 * st + 1) % kT8Values], (uint32_t)((2 * st + 1) / kT8Values) & 1u);
         };
         if (any & ~clear) {

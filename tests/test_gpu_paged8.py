@@ -498,6 +498,32 @@ def test_hidden_positions_may_hold_anything(M, rows, nq):
     assert torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(window=300, prefix=[20 + 7 * i for i in range(17)]), dict(softcap=20.0)])
+@pytest.mark.parametrize("rows,ps", [(9, 16), (16, 64), (16, 128)])
+def test_nan_behind_long_sequences_stays_hidden(M, rows, ps, kw):
+    """Codes of NaN in every position that no row sees, in units of one to 32 chunks, several segments a CTA: the last
+    chunks (and, under a window, the first) are looked over after many whose values every row sees."""
+    lens = [(977 * i) % 4001 + 1 for i in range(17)]
+    n = [1 + (i * 5) % rows for i in range(17)]
+    n[3] = rows
+    cache = R8.make_cache(lens, n, 4, ps, rows)
+    kc, vc, _, _, table, _, _ = cache
+    for b, (m, r) in enumerate(zip(lens, n)):
+        p = torch.arange(-(-(m + r) // ps) * ps, device="cuda")
+        hide = p >= m + r
+        if "window" in kw:
+            hide |= (p >= kw["prefix"][b]) & (p <= m - kw["window"])
+        p = p[hide]
+        page = table[b].long()[p // ps]
+        kc[page, :, p % ps] = 0x7F
+        vc[page, :, p % ps] = 0xFF
+    q = randn(sum(n), 16 * HD, seed=rows, scale=2.5)
+    first = attend(M, lens, n, 16, 4, ps, max_rows=rows, cache=cache, q=q, **kw)[:2]
+    for _ in range(20):
+        again = attend(M, lens, n, 16, 4, ps, max_rows=rows, cache=cache, q=q, ref=False, **kw)[:2]
+        assert all(torch.equal(x, y) for x, y in zip(first, again))
+
+
 @pytest.mark.parametrize("rows,nq", [(4, 4), (4, 8), (8, 8)])
 @pytest.mark.parametrize("what", ["value", "value scale", "key", "key scale"])
 def test_nan_is_seen_by_those_that_see_it(M, rows, nq, what):
