@@ -701,9 +701,10 @@ def _append_args(kv, k_new, v_new, row_start, ws, q, q_out, pos):
             *_workspace(ws, kv.index))
 
 
-def _is(x, what):
-    if not isinstance(x, what):
-        raise ValueError(f"expected a {what.__name__}, not a {type(x).__name__}")
+def _cache(kv, bits):
+    """Refuses a cache of the other kind, which the library would misread."""
+    if isinstance(getattr(kv, "c", None), moe_paged_kv8) is not (bits == 8):
+        raise ValueError(f"expected a cache of {bits} bits, not a {type(kv).__name__}")
 
 
 def moe_paged_kv_append(kv: PagedKV, k_new, v_new, row_start, ws, q=None, q_out=None, pos: moe_attn_pos | None = None,
@@ -711,7 +712,7 @@ def moe_paged_kv_append(kv: PagedKV, k_new, v_new, row_start, ws, q=None, q_out=
     """Appends the rows' keys and values (bf16 [T, nkv * 128], rows may be
     strided) to their sequences' pages and writes the queries to ``q_out``
     (may be ``q``), queries and keys turned by ``pos``."""
-    _is(kv, PagedKV)
+    _cache(kv, 16)
     _call("moe_paged_kv_append", kv.index, stream, lib.moe_paged_kv_append, kv._ref,
           *_append_args(kv, k_new, v_new, row_start, ws, q, q_out, pos))
 
@@ -720,8 +721,9 @@ def moe_paged_kv_append_norm(kv: PagedKV, norm: QkNorm, k_new, v_new, row_start,
                              pos: moe_attn_pos | None = None, stream=None):
     """``moe_paged_kv_append`` with the queries and keys of each head normed
     before they turn."""
-    _is(kv, PagedKV)
-    _is(norm, QkNorm)
+    _cache(kv, 16)
+    if not isinstance(norm, QkNorm):
+        raise ValueError(f"expected a QkNorm, not a {type(norm).__name__}")
     _call("moe_paged_kv_append_norm", kv.index, stream, lib.moe_paged_kv_append_norm, kv._ref, norm.ref(kv.index),
           *_append_args(kv, k_new, v_new, row_start, ws, q, q_out, pos))
 
@@ -730,7 +732,7 @@ def moe_paged_kv8_append(kv: PagedKV8, k_new, v_new, row_start, ws, q=None, q_ou
                          pos: moe_attn_pos | None = None, stream=None):
     """``moe_paged_kv_append`` to a cache of 8 bits, with ``norm`` the queries
     and keys of each head normed before they turn."""
-    _is(kv, PagedKV8)
+    _cache(kv, 8)
     _call("moe_paged_kv8_append", kv.index, stream, lib.moe_paged_kv8_append, kv._ref,
           None if norm is None else norm.ref(kv.index), *_append_args(kv, k_new, v_new, row_start, ws, q, q_out, pos))
 
@@ -754,14 +756,14 @@ def moe_paged_attention(kv: PagedKV, q, row_start, o, ws, max_rows, scores: Page
                         stream=None):
     """Attention of the rows (q, o bf16 [T, nq * 128], rows may be strided) over
     their sequences' pages; ``lse`` float32 [T, nq] or None."""
-    _is(kv, PagedKV)
+    _cache(kv, 16)
     _attention("moe_paged_attention", lib.moe_paged_attention, kv, q, row_start, o, ws, max_rows, scores, lse, stream)
 
 
 def moe_paged_kv8_attention(kv: PagedKV8, q, row_start, o, ws, max_rows, scores: PagedScores | None = None, lse=None,
                             stream=None):
     """``moe_paged_attention`` over a cache of 8 bits."""
-    _is(kv, PagedKV8)
+    _cache(kv, 8)
     _attention("moe_paged_kv8_attention", lib.moe_paged_kv8_attention, kv, q, row_start, o, ws, max_rows, scores, lse,
                stream)
 

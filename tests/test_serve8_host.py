@@ -223,6 +223,35 @@ def test_binding_refuses_tensors_it_would_misread(M):
         M.moe_paged_release(p, ints(2), ws)
 
 
+def test_a_cache_class_of_the_callers_own_is_taken(M, monkeypatch):
+    """The calls on a bf16 cache use a few attributes of it, so that any class with these will do."""
+    bf, i32 = torch.bfloat16, torch.int32
+    k = torch.zeros(6, 2, 16, 128, dtype=bf)
+    real = M.PagedKV(k, k.clone(), torch.zeros(3, 2, dtype=i32), torch.zeros(3, dtype=i32))
+
+    class Own:
+        _ref, nkv, n_seqs, index, device = real._ref, real.nkv, real.n_seqs, real.index, real.device
+
+    calls = []
+    monkeypatch.setattr(M, "_call", lambda what, index, stream, f, *args: calls.append((what, args[0])))
+    rows, q, start, ws = (torch.zeros(5, 256, dtype=bf), torch.zeros(5, 512, dtype=bf), torch.zeros(4, dtype=i32),
+                          torch.zeros(1 << 20, dtype=torch.uint8))
+    M.moe_paged_kv_append(Own(), rows, rows, start, ws)
+    M.moe_paged_attention(Own(), q, start, q, ws, 2)
+    M.moe_paged_kv_append_norm(Own(), M.QkNorm(), rows, rows, start, ws)
+    assert calls == [(n, real._ref) for n in ("moe_paged_kv_append", "moe_paged_attention", "moe_paged_kv_append_norm")]
+
+    class Own8(Own):  # a description that the bf16 calls would misread, and one that the 8-bit calls would
+        c = M.moe_paged_kv8()
+
+    for f in (lambda: M.moe_paged_kv_append(Own8(), rows, rows, start, ws), lambda: M.moe_paged_attention(Own8(), q, start, q, ws, 2),
+              lambda: M.moe_paged_kv8_append(Own(), rows, rows, start, ws), lambda: M.moe_paged_kv8_append(real, rows, rows, start, ws),
+              lambda: M.moe_paged_kv8_attention(Own(), q, start, q, ws, 2)):
+        with pytest.raises(ValueError):
+            f()
+    assert len(calls) == 3
+
+
 def test_references_round_as_the_type():
     x = torch.linspace(-448, 448, 20001, dtype=torch.float64)
     assert torch.equal(R8.encode(R8.round_e4m3(x)), x.float().to(torch.float8_e4m3fn).view(torch.uint8))
