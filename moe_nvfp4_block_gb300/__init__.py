@@ -779,14 +779,12 @@ def moe_paged_reserve(pool: PagePool, kv_len, rows, row_start, ws, slot=None, po
     ``slot`` and ``pos`` (int32, of one length) and which sequences were
     ``granted`` their pages (int32 [n_seqs])."""
     n, dev, i32 = pool.n_seqs, pool.device, torch.int32
-    T = 0 if slot is None else slot.numel()
-    if slot is None and pos is not None:
-        T = pos.numel()
+    T = max([t.numel() for t in (slot, pos) if t is not None], default=0)
     args = (_like(kv_len, i32, (n,), "kv_len", dev), _like(rows, i32, (n,), "rows", dev), T,
             _like(row_start, i32, (n + 1,), "row_start", dev))
-    # (an empty tensor has no address)
-    sp = None if T == 0 else _like(slot, i32, (T,), "slot", dev)
-    pp = None if T == 0 else _like(pos, i32, (T,), "pos", dev)
+    sp, pp = _like(slot, i32, (T,), "slot", dev), _like(pos, i32, (T,), "pos", dev)
+    if T == 0:  # an empty tensor has no address
+        sp = pp = None
     _call("moe_paged_reserve", pool.index, stream, lib.moe_paged_reserve, pool._ref, *args, sp, pp,
           _like(granted, i32, (n,), "granted", dev), *_workspace(ws, pool.index))
 

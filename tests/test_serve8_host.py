@@ -252,6 +252,26 @@ def test_a_cache_class_of_the_callers_own_is_taken(M, monkeypatch):
     assert len(calls) == 3
 
 
+def test_slots_and_positions_of_different_lengths_are_refused(M, monkeypatch):
+    ints = lambda *s: torch.zeros(s, dtype=torch.int32)
+    p = M.PagePool(ints(3, 4), ints(3), ints(10), ints(1), 16)
+    calls = []
+    monkeypatch.setattr(M, "_call", lambda what, index, stream, f, *args: calls.append(args[3:7]))
+    ws = torch.zeros(256, dtype=torch.uint8)
+    go = lambda **kw: M.moe_paged_reserve(p, ints(3), ints(3), ints(4), ws, **kw)
+    some, none = ints(5), ints(0)
+    for bad in (dict(slot=none, pos=some), dict(slot=some, pos=none), dict(slot=ints(4), pos=some), dict(slot=none.float()),
+                dict(pos=none.long()), dict(slot=none, pos=none.long()), dict(slot=ints(1, 5))):
+        with pytest.raises(ValueError):
+            go(**bad)
+    assert not calls
+    for ok, n in ((dict(slot=some, pos=some), 5), (dict(slot=some), 5), (dict(pos=some), 5), (dict(slot=none, pos=none), 0),
+                  (dict(pos=none), 0), (dict(), 0)):
+        go(**ok)
+        rows, _, slot, pos = calls.pop()
+        assert rows == n and (slot is None) == (not n or "slot" not in ok) and (pos is None) == (not n or "pos" not in ok)
+
+
 def test_references_round_as_the_type():
     x = torch.linspace(-448, 448, 20001, dtype=torch.float64)
     assert torch.equal(R8.encode(R8.round_e4m3(x)), x.float().to(torch.float8_e4m3fn).view(torch.uint8))
