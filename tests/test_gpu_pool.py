@@ -251,3 +251,25 @@ def test_on_another_stream(M):
     side.synchronize()
     s.table, s.held, s.n_free, *_ = R8.reserve(s.table, s.held, s.free, s.n_free, s.lens, [20, 20], 16, 0)
     s.same()
+
+
+@pytest.mark.parametrize("n", [64, 65, 300, 1024])
+def test_pages_without_slots_over_many_ctas(M, n):
+    """Rounds of one graph, a few pages a sequence up to hundreds, more asked for than there are in some."""
+    s = Server(M, [0] * n, 16, 300, 40 * n, seed=n)
+    rows, start = ints([0] * n), torch.zeros(n + 1, dtype=torch.int32, device="cuda")
+    M.moe_paged_reserve(s.pool, s.d["len"], rows, start, s.ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        M.moe_paged_reserve(s.pool, s.d["len"], rows, start, s.ws)
+    r = random.Random(n)
+    for step in range(4):
+        want = [r.choice([0, 1, 17, 16 * r.randint(0, 80), 4800 if step == 2 else 3]) for _ in range(n)]
+        rows.copy_(ints(want))
+        g.replay()
+        s.table, s.held, s.n_free, st, *_ = R8.reserve(s.table, s.held, s.free, s.n_free, s.lens, want, 16, 0)
+        assert start.tolist() == st
+        s.same()
+        s.release([0] * n if step == 2 else [min(16 * h, 40) for h in s.held])
+    assert s.error() in (0, CAPACITY)
