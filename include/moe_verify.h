@@ -682,7 +682,11 @@ moe_status moe_paged_reserve(const moe_page_pool* pool, const int32_t* kv_len, c
  * undoes a reserve leaves the pool as it was.  held[b] becomes kept_b where it
  * was more, the table's entries -1; kv_len is the caller's.  A sequence whose
  * pages the stack has no room for (more than n_pages in all) or with held[b]
- * outside [0, max_pages] keeps them and records MOE_ERR_INVALID_ARG.
+ * outside [0, max_pages] keeps them and records MOE_ERR_INVALID_ARG.  An entry
+ * of the table outside [0, n_pages) among the pages given back is recorded and
+ * goes to the stack as it stands, as a reserve hands it out: the pages of the
+ * stack and of the sequences stay as many as they were, and each call that
+ * moves such a page records it again.
  */
 moe_status moe_paged_release(const moe_page_pool* pool, const int32_t* keep, const int32_t* shared, void* ws,
                              size_t ws_bytes, void* stream);

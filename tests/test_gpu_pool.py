@@ -273,3 +273,21 @@ def test_pages_without_slots_over_many_ctas(M, n):
         s.same()
         s.release([0] * n if step == 2 else [min(16 * h, 40) for h in s.held])
     assert s.error() in (0, CAPACITY)
+
+
+@pytest.mark.parametrize("bad", [-1, -5, 10 ** 6, 2 ** 31 - 1])
+@pytest.mark.parametrize("n", [2, 90])
+def test_bad_pages_in_the_table_go_back_as_they_stand(M, n, bad):
+    """A release that meets them records it; so does the reserve that hands them out again, to nobody's slot."""
+    s = Server(M, [40] * n, 16, 40, 5, seed=n)
+    s.table[1][2] = bad
+    s.up()
+    s.release([40, 20] + [40] * (n - 2))
+    assert s.error() == INVALID and s.free[5] == bad and s.n_free == 6 and s.held[1] == 2
+    s.lens[1] = 20
+    s.d["len"].copy_(ints(s.lens))
+    _, slot, _ = s.reserve([0, 20] + [0] * (n - 2), 23)
+    assert s.error() == INVALID and s.table[1][2] == bad
+    assert (slot[:12] >= 0).all() and (slot[12:] == -1).all()
+    s.release([0] * n)
+    assert s.error() == INVALID and s.n_free == 5 + 3 * n and s.free.count(bad) == 1 + (bad == -1) * (len(s.free) - s.n_free)
