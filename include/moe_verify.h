@@ -599,7 +599,11 @@ typedef struct {
  * positions are in it (rows that were rejected may leave it larger than what
  * they leave behind needs), and a block whose first position is new starts
  * afresh, whatever its page held.
- * q, q_out as in moe_paged_kv_append (bf16).  ws, ws_bytes as there.
+ * q, q_out as in moe_paged_kv_append (bf16), but that sines and cosines are
+ * taken more exactly here (their FP32 values off by little more than half an
+ * ulp and what the frequency's and the angle's rounding to double, 2^-52 of
+ * the angle, moves them by), so that a turned query may come out with another last bit than there.  ws,
+ * ws_bytes as there.
  */
 moe_status moe_paged_kv8_append(const moe_paged_kv8* kv, const moe_qk_norm* norm, const uint16_t* q, int64_t q_stride,
                                 const uint16_t* k_new, int64_t k_stride, const uint16_t* v_new, int64_t v_stride,
@@ -652,7 +656,12 @@ size_t moe_page_pool_workspace_size(void);
  * a sequence with grow_b = 0 or end_b <= *n_free is granted its pages: the
  * k-th page of the call is free_pages[*n_free - 1 - k], at table[b][held[b] ..].
  * Another one gets none (MOE_ERR_CAPACITY is recorded) and keeps what it has;
- * so does one with need_b > max_pages, whose grow_b counts as 0.
+ * so does one with need_b > max_pages, whose grow_b counts as 0.  The rows of
+ * a sequence that is not granted count in row_start all the same: an append
+ * stores those that fall into pages it holds (in a cache of 8 bits the scale of
+ * its last block may grow with them) and records the others, an attention
+ * leaves the sequence's rows undefined.  The same step serves it once there are
+ * pages.  (rows[b] = 0 keeps it out.)
  *   row_start  int32 [n_seqs + 1] out: 0 and the running sums of rows, what the
  *              paged calls take
  *   slot, pos  int32 [n_rows] out, or NULL: for row t of sequence b its position

@@ -313,6 +313,56 @@ def test_appends_in_steps_and_again(M):
     assert bool(((got - x.double()).abs() <= room).all())
 
 
+def test_row_starts_that_fall(M):
+    """The second sequence's rows are wrong; the third's two lie within the first's seven, which has the other five."""
+    lens = [20, 33, 14]
+    kc, vc, ks, vs, table, length, _ = R8.make_cache(lens, [7, 4, 2], 2, 16, 1, spare=0)
+    x = randn(9, 4 * HD, seed=5)
+    x[3] *= 64  # (the largest: not the first sequence's)
+    kv = M.PagedKV8(kc, vc, ks, vs, table, length)
+    ws = M.paged_workspace(kv, 1, 2)
+    before = [t.clone() for t in (kc, ks, vc, vs)]
+    o = torch.full_like(x, 5.0)
+    M.moe_paged_kv8_append(kv, x[:, :2 * HD], x[:, 2 * HD:], ints([0, 7, 3, 5]), ws, q=x, q_out=o)
+    assert M.moe_workspace_error(ws) == INVALID
+    assert torch.equal(o[:7], x[:7]) and bool((o[7:] == 5.0).all())
+    pos = 20 + torch.arange(3, 5, device="cuda")
+    gap = table[0].long()[pos // 16], slice(None), pos % 16
+    for codes, scale, old, old_scale, cols in ((kc, ks, before[0], before[1], slice(0, 2 * HD)),
+                                               (vc, vs, before[2], before[3], slice(2 * HD, 4 * HD))):
+        y = x[:, cols].double().unflatten(1, (-1, HD))
+        first = y[:7].clone()
+        first[3:5] = 0
+        want, want_scale, _ = R8.store(old, old_scale, table, lens, [7, 0, 2], 16, torch.cat([first, y[3:5]]))
+        want[gap] = old[gap]  # what the first sequence's rows leave free stays
+        assert torch.equal(codes, want) and torch.equal(scale, want_scale)
+
+
+@pytest.mark.parametrize("big", [1.0, 64.0, 2.0 ** 14, 2.0 ** 30])
+def test_rounds_of_rejected_outliers(M, big):
+    """Three of four rows are rejected each round, `big` times the committed ones: the cache is what the rule gives, and
+    what is committed is off by its rounding and, of blocks whose scale has grown, by half a step of the last scale's
+    smallest at each growth."""
+    kc, vc, ks, vs, table, length, _ = R8.make_cache([0], [70], 2, 16, 1)
+    kv = M.PagedKV8(kc, vc, ks, vs, table, length)
+    ws = M.paged_workspace(kv, 1, 2)
+    x = randn(64, 4, 2 * HD, seed=5)
+    x[:, 1:] *= big
+    for t in range(64):
+        length.fill_(t)
+        before = kc.clone(), ks.clone()
+        M.moe_paged_kv8_append(kv, x[t], x[t], ints([0, 4]), ws)
+        want = R8.store(*before, table, [t], [4], 16, x[t].double().unflatten(1, (-1, HD)))
+        assert torch.equal(kc, want[0]) and torch.equal(ks, want[1])
+    assert M.moe_workspace_error(ws) == 0
+    p = torch.arange(64, device="cuda")
+    page, slot = table[0].long()[p // 16], p % 16
+    got, y = R8.decode(kc, ks)[page, :, slot].flatten(1), x[:, 0].double()
+    s = torch.exp2(ks.double() - 127)[page, :, slot // 16].repeat_interleave(HD, -1)
+    # (a scale grows by whole powers of two: roundings of half steps 2^-10 s, s/2, s/4 .. add up to less than 2^-9 s)
+    assert bool(((got - y).abs() <= 2.0 ** -4 * y.abs() + 2.0 ** -9 * s).all())
+
+
 # ---------------------------------------------------------------- the normed append to the bf16 cache
 
 @pytest.mark.parametrize("nq,nkv", [(32, 8), (1, 1), (48, 8), (10, 5), (6, 2)])
@@ -848,3 +898,64 @@ def test_serving_rounds(M, ps, nq):
     M.moe_paged_release(pool, ints([0] * n), ws)
     assert n_free.tolist() == [pages] and sorted(free.tolist()) == list(range(pages))
     assert bool((table == -1).all()) and M.moe_workspace_error(ws) == 0
+
+
+@pytest.mark.parametrize("ps", [16, 64])
+@pytest.mark.parametrize("nq", [8, 16])
+def test_serving_with_a_pool_that_runs_short(M, ps, nq):
+    """A captured step (reserve, append, attention) in which two of four sequences get no page: the others are served and
+    every cache is as it should be; with pages back, the same step serves all."""
+    nkv, width, pages, K = 2, 8, 40, 4
+    lens, T, w = [2 * ps - 2, 4 * ps - 2, 3 * ps - 2, ps + 4], 16, nq + 2 * nkv
+    kc, vc = (torch.zeros(pages, nkv, ps, HD, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros(pages, nkv, ps // 16, dtype=torch.uint8, device="cuda") for _ in range(2))
+    table = torch.full((4, width), -1, dtype=torch.int32, device="cuda")
+    length, held, free = ints([0] * 4), ints([0] * 4), torch.randperm(pages, device="cuda").int()
+    n_free, rows, start, granted = ints([pages]), ints(lens), ints([0] * 5), ints([0] * 4)
+    pool, kv = M.PagePool(table, held, free, n_free, ps), M.PagedKV8(kc, vc, ks, vs, table, length)
+    ws, f = M.paged_workspace(kv, K, nq), freqs("whole")
+    gain = (1 + 0.3 * randn(HD, seed=3).float()).bfloat16()
+    nm, pos = M.QkNorm(gain, gain, 1e-6), M.attn_pos(rotary_dim=HD)
+    x0 = randn(sum(lens), w * HD, seed=1)
+    M.moe_paged_reserve(pool, length, rows, start, ws, granted=granted)
+    M.moe_paged_kv8_append(kv, x0[:, nq * HD:(nq + nkv) * HD], x0[:, (nq + nkv) * HD:], start, ws, norm=nm, pos=pos)
+    assert granted.tolist() == [1] * 4 and held.tolist() == [2, 4, 3, 2] and M.moe_workspace_error(ws) == 0
+    length.copy_(ints(lens))
+    rows.fill_(K)
+    x = randn(T, w * HD, seed=2)
+    q, k, v = x[:, :nq * HD], x[:, nq * HD:(nq + nkv) * HD], x[:, (nq + nkv) * HD:]
+    qt, o, slot = torch.zeros(T, nq * HD, dtype=torch.bfloat16, device="cuda"), torch.zeros(T, nq * HD, dtype=torch.bfloat16, device="cuda"), ints([0] * T)
+
+    def step():
+        M.moe_paged_reserve(pool, length, rows, start, ws, slot=slot, granted=granted)
+        M.moe_paged_kv8_append(kv, k, v, start, ws, q=q, q_out=qt, norm=nm, pos=pos)
+        M.moe_paged_kv8_attention(kv, qt, start, o, ws, K)
+
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        step()
+    nk = R8.new_rows(k, torch.cat([n + torch.arange(K, device="cuda") for n in lens]), f, gain, 1e-6)
+    nv = v.double().unflatten(1, (-1, HD))
+    left = int(n_free)
+    for have, ok in ((1, [1, 0, 0, 1]), (left - 1, [1, 1, 1, 1])):
+        n_free.fill_(have)
+        before = [t.clone() for t in (kc, ks, vc, vs)]
+        g.replay()
+        assert M.moe_workspace_error(ws) == (0 if all(ok) else CAPACITY)
+        assert granted.tolist() == ok and start.tolist() == [0, 4, 8, 12, 16]
+        # a sequence without its page: its rows go as far as the pages it holds
+        stored = [K if y else 2 for y in ok]
+        mine = torch.cat([4 * b + torch.arange(r, device="cuda") for b, r in enumerate(stored)])
+        check_pool(kc, ks, before[0], *R8.store(before[0], before[1], table, lens, stored, ps, nk[mine]), nk, False, "keys")
+        check_pool(vc, vs, before[2], *R8.store(before[2], before[3], table, lens, stored, ps, nv[mine]), nv, True, "values")
+        want = R8.attention(qt, R8.decode(kc, ks), R8.decode(vc, vs), R8.scales(vs), table, lens, [K] * 4, nq)
+        served = torch.cat([4 * b + torch.arange(K, device="cuda") for b in range(4) if ok[b]])
+        R8.check_attention(o[served], None, tuple(t[served] for t in want), f"{ok}")
+        for b in range(4):
+            p = lens[b] + torch.arange(K, device="cuda")
+            assert slot[4 * b:4 * b + 4].tolist() == ((table[b].long()[p // ps] * ps + p % ps).tolist() if ok[b] else [-1] * K)
+        if have == 1:
+            assert n_free.tolist() == [0] and held.tolist() == [3, 4, 3, 2]
+            free.copy_(torch.roll(free, -1))  # the others come back
+    assert held.tolist() == [3, 5, 4, 2]
