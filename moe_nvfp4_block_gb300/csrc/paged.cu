@@ -44,8 +44,11 @@ constexpr int kApRows = 4;  // most rows of a CTA
 // NORM: the queries and keys of each head are divided by the root of their mean
 // square (over the head's lanes by shuffles) and multiplied by the gain (in
 // shared memory: in registers, 16 dims a lane, fewer CTAs fit), before they turn;
-// all in FP32.  8247 rows of 80 heads: 85 us, 4.0 TB/s read and written
-// (instructions: 53% of the issue slots); 160 verify rows of 48 heads 4.4 us.
+// all in FP32.  8247 rows of 80 heads: 85 us, 4.0 TB/s read and written (a step's
+// two heads are used as soon as loaded: waits for loads are the first stall, then
+// instructions, 53% of the issue slots); 160 verify rows of 48 heads 4.5 us.
+// Widths whose half is no multiple of 8 cost twice: 8240 rows of 64 heads with 60
+// rotary dims 117 us, with 64 57 (norms: 118, 63).
 template <bool VEC, bool NORM>
 __global__ void __launch_bounds__(kApThreads, NORM ? 4 : 0) k_paged_append(const __grid_constant__ PagedAppendArgs a) {
   constexpr int U = 2;

@@ -7,8 +7,8 @@
 // 128-position chunk (32 KB)
 //   S [rows, 128]  = Q K^T   8 tcgen05.mma kind::f8f6f4 M128 N128 K32: K as it lies
 //                            in the page, Q as two E4M3 parts (hi + lo) of its rows
-//                            scaled to below 2^8: exact down to 2^-10 of the row's
-//                            largest value, and to 2^-18 of that below.  Q is in
+//                            scaled to below 2^8: exact down to 2^-9 of the row's
+//                            largest value, and to 2^-17 of that below.  Q is in
 //                            tensor memory, each row twice: a row's two lanes
 //                            (threads) take half of the positions each
 //   O^T [128, rows] += V^T P^T   8 tcgen05.mma kind::f16 M128 N64 K16: P as in
@@ -22,13 +22,12 @@
 // Measured: 65,003 and 131,001 positions, 8 KV heads of 64 query rows, 402 MB:
 // 92 to 93 us (4.3 TB/s; the bf16 cache 132); 19 sequences of 4096 with 64 rows
 // 46 us (58), with a softcap 78, with a bias by distance 73; 64 ragged sequences
-// of 64 rows 137; 608 units of one chunk 35.  What is left is instructions and
-// their fetching: 15 warps of five kinds share an SM's instruction cache, and what
-// is taken out of their loops (a copy that knew whole chunks of plain scores only
-// had 86) or laid out another way moves the time by as much as any step of
-// arithmetic.  The producer takes 1900 clocks a chunk, near the chunk's own time
-// (its scales by a 16th warp: 100 us).  The tensor pipe is busy in 39% of the
-// cycles.  Slower, too: 16 softmax warps (80 registers a thread: spills), chunks of
+// of 64 rows 137; 608 units of one chunk 35.  What paces a chunk is its one producer
+// warp: it takes 1900 clocks of the chunk's 2150 (81 chunks a CTA), its scales' eight
+// lanes of work with all 32 (by a 16th warp: 100 us).  Instructions come second: 15
+// warps of five kinds share an SM's instruction cache (97% hits, an issue in 49% of
+// the cycles), and a copy that knew whole chunks of plain scores only had 86, 7%
+// less.  The tensor pipe is busy in 39% of the cycles.  Slower, too: 16 softmax warps (80 registers a thread: spills), chunks of
 // 64 positions (half the work between the same waits), one pass over the scores with
 // the last maximum, weights formed again where it grows (130: the next S waits for
 // it), exponentials unrolled twice as far (101), rows of Q by the softmax warps (131).

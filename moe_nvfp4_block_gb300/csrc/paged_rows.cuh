@@ -52,8 +52,10 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
-// Cosine and sine of p f, each to little more than half an ulp, so that E4M3
-// codes are as far off as their rounding alone: the angle less its multiple of
+// Cosine and sine of p f, each to little more than half an ulp and what the
+// product's rounding moves the angle by (2^-53 of it: 1.5e-11 at 131,072, which
+// counts only near a zero, and 2.4e-7 at 2^31), so that E4M3 codes are as far off
+// as their rounding alone: the angle less its multiple of
 // pi / 2 in double, as hi + lo in FP32; the Taylor series of sin and cos up to
 // hi^9 and hi^10 (|hi| <= pi / 4: what follows is below 2^-28), their leading
 // terms' rounding errors kept apart until the last sum; lo to first order.
